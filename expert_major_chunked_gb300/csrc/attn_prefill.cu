@@ -184,6 +184,11 @@ constexpr uint64_t kWaitNs = 2000000000ull;
 // have the room, and o is multiplied (a pass over TMEM) only then. The choice is each row's own, so a row's bits do not
 // depend on the rows beside it.
 constexpr float kSlack = 8.0f;
+// log2 of the weight at the reference maximum. f16 is normal from 2^-14 to 2^16: with 2^7 there, and 2^8 more while the
+// reference lags, the largest weight is from 2^7 to 2^15 and a weight keeps its 11 bits down to 2^-21 of it (with 1 there,
+// down to 2^-14 only). bf16 has float32's exponents, so its weights keep their bits wherever they lie.
+template <class T>
+constexpr float kTop = T::kCode == 1 ? 7.0f : 0.0f;
 
 template <int D>
 struct Tc {
@@ -736,7 +741,7 @@ __global__ void __launch_bounds__(kTThreads, 1) prefill_kernel(const __grid_cons
             m = mn;
           }
           const float u = m == -INFINITY ? 0.0f : m;
-          const float2 c2 = make_float2(c, c), u2 = make_float2(-u, -u);
+          const float2 c2 = make_float2(c, c), u2 = make_float2(kTop<T> - u, kTop<T> - u);
           float2 sum[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) sum[i] = make_float2(0.0f, 0.0f);
@@ -815,7 +820,8 @@ __global__ void __launch_bounds__(kTThreads, 1) prefill_kernel(const __grid_cons
         bad |= !(zero.x == 0.0f && zero.y == 0.0f);
         ptx::tc_fence_before();
         if (real && a.lse)
-          a.lse[static_cast<int64_t>(h) * a.total_q + t.at.q0 + tok] = l > 0.0f ? (m + log2_fast(l)) * kLn2 : -INFINITY;
+          a.lse[static_cast<int64_t>(h) * a.total_q + t.at.q0 + tok] =
+              l > 0.0f ? (m - kTop<T> + log2_fast(l)) * kLn2 : -INFINITY;
         uint32_t again = __ballot_sync(~0u, bad && real);
         const uint16_t* k = static_cast<const uint16_t*>(a.k) + t.at.k0 * a.k_token + t.at.kvh * a.k_head;
         const uint16_t* v = static_cast<const uint16_t*>(a.v) + t.at.k0 * a.v_token + t.at.kvh * a.v_head;
