@@ -58,6 +58,10 @@ __device__ __forceinline__ int request_len(const moe_attn_decode_args& a, int b)
   const long long cap = static_cast<long long>(a.max_blocks) * a.block_size;
   return static_cast<int>(min(static_cast<long long>(max(a.kv_lens[b], 0)), cap));
 }
+// len / n rounded up; a length may be 2^31 - 1, so the sum is taken without a sign
+__device__ __forceinline__ int parts_of(int len, int n) {
+  return static_cast<int>((static_cast<uint32_t>(len) + static_cast<uint32_t>(n - 1)) / static_cast<uint32_t>(n));
+}
 
 // the first unit of range i of `ranges` (a 64-bit division takes several hundred cycles; few calls need one)
 __device__ __forceinline__ long long first_unit(long long total, long long ranges, uint32_t i) {
@@ -107,7 +111,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) decode_kernel(const __grid_con
   // this CTA's range of units, and the request that it begins in
   const int per = (a.n_requests + kDecThreads - 1) / kDecThreads;
   const int b_lo = min(a.n_requests, tid * per), b_hi = min(a.n_requests, b_lo + per);
-  auto tiles_of = [&](int b) { return (request_len(a, b) + CT - 1) / CT; };
+  auto tiles_of = [&](int b) { return parts_of(request_len(a, b), CT); };
   long long mine = 0;
   for (int b = b_lo; b < b_hi; ++b) mine += tiles_of(b);
   long long incl = mine;
@@ -149,7 +153,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) decode_kernel(const __grid_con
   const int g = lane >> 2, t4 = lane & 3;
 
   while (u < u_end) {
-    const int len = request_len(a, b), nt = (len + CT - 1) / CT;
+    const int len = request_len(a, b), nt = parts_of(len, CT);
     const long long n_units = static_cast<long long>(nt) * geo.units_per_tile;
     if (u >= base + n_units) {
       base += n_units;
@@ -163,16 +167,16 @@ __global__ void __launch_bounds__(kDecThreads, 2) decode_kernel(const __grid_con
     const int tiles = static_cast<int>(min(static_cast<long long>(nt - first), u_end - u));
     const int kvh = hs / geo.slices, row0 = (hs % geo.slices) * geo.rows, rows = min(geo.rows, geo.group - row0);
     const int h0 = kvh * geo.group + row0;
-    const int tok_end = min(len, (first + tiles) * CT);
+    const int tok_end = static_cast<int>(min(static_cast<uint32_t>(len), static_cast<uint32_t>(first + tiles) * CT));
     const int32_t* table = a.block_table + b * a.table_stride;
 
     // the stage ring: a warp takes every fourth chunk of the segment
     int next_chunk = first * kDecWarps + warp, chunk = next_chunk, fill = 0, take = 0;
-    const int chunk_end = (tok_end + TOK - 1) / TOK;
+    const int chunk_end = parts_of(tok_end, TOK);
     auto block_of = [&](int c) {  // lanes below TT: the block of 16 tokens each
-      const int tok = c * TOK + lane * 16;
+      const uint32_t tok = static_cast<uint32_t>(c) * TOK + lane * 16;  // (c may lie past the end)
       int id = -1;
-      if (lane < TT && tok < tok_end) {
+      if (lane < TT && tok < static_cast<uint32_t>(tok_end)) {
         id = table[tok >> block_log2];
         if (id < 0 || id >= a.num_blocks) id = -1;
       }
@@ -274,7 +278,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) decode_kernel(const __grid_con
       const uint32_t st = stage0 + take * kStageBytes;
       const float* sc_sh = scale_sh[warp][take];
       take = take + 1 == kDecStages ? 0 : take + 1;
-      bool full = (chunk + 1) * TOK <= tok_end;
+      bool full = static_cast<uint32_t>(chunk + 1) * TOK <= static_cast<uint32_t>(tok_end);
 #pragma unroll
       for (int i = 0; i < TT; ++i) full &= sc_sh[4 + i] > 0.0f;  // a block outside the cache left zeros
       float s[TT][NH][4];
