@@ -368,7 +368,7 @@ __global__ void __launch_bounds__(kTThreads, 1) prefill_kernel(const __grid_cons
     *abort_flag = 0;
     ptx::fence_barrier_init();
   }
-  if (warp == 8 && lane == 0) {
+  if (warp == 8 && lane == 0 && a.total_k > 0) {  // (without keys there are no such maps)
     ptx::tma_prefetch_desc(&p.k);
     ptx::tma_prefetch_desc(&p.v);
   }
@@ -908,7 +908,6 @@ cudaError_t launch_tiles(const moe_attn_prefill_args& a, cudaStream_t stream) {
   // sequences begin new tiles, so there are at most total / tokens + n_seqs
   const int64_t tiles = (static_cast<int64_t>(a.total_q) / (C::NQ * sub_tokens) + a.n_seqs) * a.n_kv_heads * p.slices;
   return launch_early(prefill_kernel<T, D>, dim3(static_cast<unsigned>(tiles)), dim3(kTThreads), C::SMEM, stream, p);
-  return cudaGetLastError();
 }
 
 }  // namespace

@@ -24,3 +24,15 @@ def test_decode_lengths_up_to_the_last_int32(d, columns):
     out, lse = attention.decode(q, dev, table, kv.ints([top, 100]))
     want = ref.decode(q, kc, vc, ks, vs, small.cpu(), [2 * bs - 1, 100], 1 / math.sqrt(d))
     ref.check(out, lse.T, want, ref.U[torch.float16])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_prefill_without_any_keys(d, dtype):
+    """Queries and not one key in the call: zeros and lse = -inf."""
+    from expert_major_chunked_gb300 import attention
+    q, none = torch.ones(70, 4, d, dtype=dtype, device="cuda"), torch.empty(0, 2, d, dtype=dtype, device="cuda")
+    out, lse = torch.full_like(q, 7.0), torch.full((4, 70), 7.0, device="cuda")
+    attention.prefill(q, none, none, kv.ints([0, 30, 30, 70]), kv.ints([0, 0, 0, 0]), out=out, lse=lse)
+    attention.raise_on_device_error()
+    assert not out.any() and (lse == -math.inf).all()
