@@ -32,6 +32,17 @@ __device__ __forceinline__ void seq_bounds(const int32_t* cu, int b, int total, 
   len = max(min(max(cu[b + 1], 0), total) - start, 0);
 }
 
+// A CTA's flags in shared memory: abort is raised by a wait that gives up and ends the others; worked is when the CTA last
+// got on with its work (another tile, and once in kNote steps of keys, of the search for a tile, or keys of a row
+// done by loops, of a microsecond or less each). A tile may have millions of steps, and most roles wait for most of it, so
+// how long a wait takes says nothing by itself.
+struct Flags {
+  uint64_t worked;
+  int abort;
+};
+constexpr int kNote = 1024;
+__device__ __forceinline__ void note_work(volatile Flags* f) { f->worked = ptx::globaltimer(); }
+
 // A tile of work: `tokens` tokens of a sequence from tok0 on, for a slice of the query heads of a kv head.
 struct TileAt {
   int valid, q0, q_len, k0, k_len, tok0, kvh, slice;
@@ -43,12 +54,13 @@ struct TileAt {
 // step of the search. The (kv head, slice) units of a tile come one after the other. One warp, all lanes.
 struct TileOrder {
   const moe_attn_prefill_args& a;
+  volatile Flags* flags;
   int tokens, units, slices;
   int q0, q_len, k0, k_len, n_tiles, level0;  // this lane's sequence (up to 32 sequences)
   int total;                                   // tiles of all sequences
 
-  __device__ TileOrder(const moe_attn_prefill_args& args, int tokens_, int slices_)
-      : a(args), tokens(tokens_), units(args.n_kv_heads * slices_), slices(slices_) {
+  __device__ TileOrder(const moe_attn_prefill_args& args, volatile Flags* flags_, int tokens_, int slices_)
+      : a(args), flags(flags_), tokens(tokens_), units(args.n_kv_heads * slices_), slices(slices_) {
     const int lane = threadIdx.x & 31;
     total = 0;
     for (int b0 = 0; b0 < a.n_seqs; b0 += 32) {
@@ -59,6 +71,7 @@ struct TileOrder {
       }
       n_tiles = (q_len + tokens - 1) / tokens;
       total += __reduce_add_sync(~0u, n_tiles);
+      if (lane == 0 && (b0 / 32) % kNote == kNote - 1) note_work(flags);
     }
     const int shift = k_len - q_len;
     level0 = shift >= 0 ? shift / tokens : -((-shift + tokens - 1) / tokens);
@@ -109,6 +122,7 @@ struct TileOrder {
           break;
         }
         left -= __shfl_sync(~0u, incl, 31);
+        if (lane == 0 && (b0 / 32) % kNote == kNote - 1) note_work(flags);
       }
     }
     t.valid = 1;
@@ -123,7 +137,8 @@ struct TileOrder {
 // hidden key or value that is NaN or infinite may have been multiplied by a probability of zero. One warp.
 template <class T, int D>
 __device__ __noinline__ void row_by_loops(const uint16_t* q, const uint16_t* k, int64_t k_token, const uint16_t* v,
-                                          int64_t v_token, int keys, float c, uint16_t* out, float* lse) {
+                                          int64_t v_token, int keys, float c, uint16_t* out, float* lse,
+                                          volatile Flags* flags) {
   constexpr int W = D / 64;
   const int lane = threadIdx.x & 31;
   float2 qf[W], o[W];
@@ -143,6 +158,7 @@ __device__ __noinline__ void row_by_loops(const uint16_t* q, const uint16_t* k, 
 #pragma unroll
     for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(~0u, s, d);
     s *= c;
+    if (lane == 0 && j % kNote == kNote - 1) note_work(flags);
     const float mn = s > m || !(s == s) ? s : m;  // a NaN score makes the row NaN
     const float ms = mn == -INFINITY ? 0.0f : mn;
     const float f = exp2_fast(m - ms), p = exp2_fast(s - ms);
@@ -179,7 +195,7 @@ constexpr int kTKeys = 128, kTRows = 128, kTThreads = 384;
 // Steps before a tile's end at which the next one is asked for: late enough that it is not promised long before it can
 // start (asked for at once: 63 us against 54 on 3001 tokens at head_dim 256), early enough for its first loads.
 constexpr int kSoon = 2;
-constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr int64_t kWaitNs = 2000000000;  // a wait gives up when nothing of its CTA has advanced for this long
 // A row keeps its reference maximum until a score passes it by more than 2^8: the sums and the 16-bit probabilities
 // have the room, and o is multiplied (a pass over TMEM) only then. The choice is each row's own, so a row's bits do not
 // depend on the rows beside it.
@@ -211,8 +227,18 @@ struct TcParams {
   int32_t heads_per_tile, slices;
 };
 
-__device__ __forceinline__ void raise_wait(volatile int* abort_flag, int site) {
-  *abort_flag = 1;
+__device__ __forceinline__ bool wait_working(uint32_t bar, uint32_t parity, volatile Flags* f) {
+  for (uint32_t it = 0;; ++it) {
+    if (ptx::mbar_try_wait(bar, parity)) return true;
+    if ((it & 15u) == 15u) {
+      const uint64_t since = f->worked;
+      if (f->abort || static_cast<int64_t>(ptx::globaltimer() - since) > kWaitNs) return false;
+    }
+  }
+}
+
+__device__ __forceinline__ void raise_wait(volatile Flags* f, int site) {
+  f->abort = 1;
   atomicCAS(&g_attn_error, 0, site);
 }
 
@@ -333,16 +359,16 @@ __global__ void __launch_bounds__(kTThreads, 1) prefill_kernel(const __grid_cons
                  rec_empty = rec_full + 16u, drain = rec_empty + 16u, taken = drain + 8u, soon = taken + 8u;
   const uint32_t answer = bars + 448u;  // 16 bytes: the tile taken over from a CTA that has not started
   uint8_t* tail = smem_raw + (soon + 8u - raw);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tail);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(tail + 4);
-  volatile TileAt* records = reinterpret_cast<volatile TileAt*>(tail + 8);  // [2]
-  static_assert(8 * (2 * C::STAGES + 17) + 8 + 2 * sizeof(TileAt) <= 448, "barriers and records");
+  volatile Flags* flags = reinterpret_cast<volatile Flags*>(tail);
+  volatile TileAt* records = reinterpret_cast<volatile TileAt*>(tail + sizeof(Flags));  // [2]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tail + sizeof(Flags) + 2 * sizeof(TileAt));
+  static_assert(8 * (2 * C::STAGES + 17) + sizeof(Flags) + 2 * sizeof(TileAt) + 4 <= 448, "barriers and records");
   const int warp = __shfl_sync(~0u, static_cast<int>(threadIdx.x) >> 5, 0), lane = static_cast<int>(threadIdx.x) & 31;
   const int group = a.n_heads / a.n_kv_heads, hpt = p.heads_per_tile, sub_tokens = kTRows / hpt;
 
   if (warp == 10) {  // the first tile's record, beside the set-up below
     wait_for_previous();
-    const TileOrder order(a, NQ * sub_tokens, p.slices);
+    const TileOrder order(a, flags, NQ * sub_tokens, p.slices);
     TileAt t{};
     order.find(blockIdx.x, t);
     if (lane == 0) write_record(records[0], t);
@@ -365,7 +391,7 @@ __global__ void __launch_bounds__(kTThreads, 1) prefill_kernel(const __grid_cons
     ptx::mbar_init(drain, 1);
     ptx::mbar_init(taken, 1);
     ptx::mbar_init(soon, 1);
-    *abort_flag = 0;
+    flags->abort = 0;
     ptx::fence_barrier_init();
   }
   if (warp == 8 && lane == 0 && a.total_k > 0) {  // (without keys there are no such maps)
@@ -377,6 +403,7 @@ __global__ void __launch_bounds__(kTThreads, 1) prefill_kernel(const __grid_cons
   if (warp == 9) {      // (after the wait: a CTA of that work that has yet to ask for its TMEM comes first)
     ptx::tmem_alloc(ptx::smem_u32(tmem_slot), 512);
     ptx::tmem_relinquish();
+    if (lane == 0) note_work(flags);  // (all that the CTA has waited for so far was other work)
   }
   ptx::tc_fence_before();
   __syncthreads();
@@ -389,8 +416,8 @@ __global__ void __launch_bounds__(kTThreads, 1) prefill_kernel(const __grid_cons
     int n_tok[NQ], n_keys[NQ], most;
   };
   auto read_tile = [&](int it, Tile& t) {  // false: no more tiles (or a wait gave up)
-    if (!ptx::wait_bounded(rec_full + 8u * (it & 1), (it >> 1) & 1, kWaitNs, abort_flag)) {
-      raise_wait(abort_flag, 4);
+    if (!wait_working(rec_full + 8u * (it & 1), (it >> 1) & 1, flags)) {
+      raise_wait(flags, 4);
       return false;
     }
     const volatile TileAt& r = records[it & 1];
@@ -425,8 +452,8 @@ __global__ void __launch_bounds__(kTThreads, 1) prefill_kernel(const __grid_cons
 #pragma unroll
             for (int part = 0; part < C::PARTS; ++part) {
               const uint32_t stage = issued % C::STAGES, use = issued / C::STAGES;
-              if (failed || !ptx::wait_bounded(empty0 + 8u * stage, (use & 1u) ^ 1u, kWaitNs, abort_flag)) {
-                if (!failed) raise_wait(abort_flag, 1);
+              if (failed || !wait_working(empty0 + 8u * stage, (use & 1u) ^ 1u, flags)) {
+                if (!failed) raise_wait(flags, 1);
                 failed = true;
                 return;
               }
@@ -451,7 +478,7 @@ __global__ void __launch_bounds__(kTThreads, 1) prefill_kernel(const __grid_cons
         for (uint32_t s = 0; s < C::STAGES; ++s) {
           const uint32_t n = issued / C::STAGES + (s < issued % C::STAGES ? 1u : 0u);
           if (n) ptx::wait_bounded(full0 + 8u * s, (n - 1u) & 1u, kWaitNs, &no_abort);
-          if (n && !failed) ptx::wait_bounded(empty0 + 8u * s, (n - 1u) & 1u, kWaitNs, abort_flag);
+          if (n && !failed) wait_working(empty0 + 8u * s, (n - 1u) & 1u, flags);
         }
       }
       __syncwarp();
@@ -464,8 +491,8 @@ __global__ void __launch_bounds__(kTThreads, 1) prefill_kernel(const __grid_cons
         for (int it = 0; read_tile(it, t); ++it) {
           done_reading(it);
           if (t.most == 0) continue;
-          if (!ptx::wait_bounded(q_empty, (n & 1u) ^ 1u, kWaitNs, abort_flag)) {
-            raise_wait(abort_flag, 5);
+          if (!wait_working(q_empty, (n & 1u) ^ 1u, flags)) {
+            raise_wait(flags, 5);
             failed = true;
             break;
           }
@@ -478,14 +505,14 @@ __global__ void __launch_bounds__(kTThreads, 1) prefill_kernel(const __grid_cons
         }
         int no_abort = 0;
         if (n) ptx::wait_bounded(q_full, (n - 1u) & 1u, kWaitNs, &no_abort);
-        if (n && !failed) ptx::wait_bounded(q_empty, (n - 1u) & 1u, kWaitNs, abort_flag);
+        if (n && !failed) wait_working(q_empty, (n - 1u) & 1u, flags);
       }
       __syncwarp();
     } else if (warp == 10) {
       // ------------------------------------------------------------ which tile comes next
       // The grid has a CTA for every tile, longest first. One CTA an SM starts; when it is ready for another tile it takes
       // one over from a CTA that has not started, so the next tile always goes to the first CTA that is free.
-      const TileOrder order(a, NQ * sub_tokens, p.slices);
+      const TileOrder order(a, flags, NQ * sub_tokens, p.slices);
       if (lane == 0) ptx::mbar_arrive(rec_full);
       uint32_t asked = 0, index = 0;
       bool more = true;     // there may be CTAs that have not started
@@ -495,18 +522,19 @@ __global__ void __launch_bounds__(kTThreads, 1) prefill_kernel(const __grid_cons
           take_over(answer, taken);
         }
         __syncwarp();
-        if (!__all_sync(~0u, ptx::wait_bounded(taken, asked++ & 1u, kWaitNs, abort_flag))) return false;
+        if (!__all_sync(~0u, wait_working(taken, asked++ & 1u, flags))) return false;
         more = took_over(answer, index);
+        if (lane == 0) note_work(flags);
         ptx::fence_proxy_async_smem();  // the answer's place may be written again
         __syncwarp();
         return true;
       };
       bool have = records[0].valid != 0, ok = true;
       for (int it = 1; have; ++it) {
-        ok = __all_sync(~0u, ptx::wait_bounded(rec_empty + 8u * (it & 1), ((it >> 1) & 1) ^ 1, kWaitNs, abort_flag)) &&
-             __all_sync(~0u, ptx::wait_bounded(soon, (it - 1) & 1, kWaitNs, abort_flag)) && ask();
+        ok = __all_sync(~0u, wait_working(rec_empty + 8u * (it & 1), ((it >> 1) & 1) ^ 1, flags)) &&
+             __all_sync(~0u, wait_working(soon, (it - 1) & 1, flags)) && ask();
         if (!ok) {
-          if (lane == 0) raise_wait(abort_flag, 6);
+          if (lane == 0) raise_wait(flags, 6);
           break;
         }
         TileAt t{};
@@ -531,8 +559,8 @@ __global__ void __launch_bounds__(kTThreads, 1) prefill_kernel(const __grid_cons
         bool failed = false;
         auto wait = [&](uint32_t bar, uint32_t parity) {
           if (failed) return false;
-          if (!__all_sync(~0u, ptx::wait_bounded(bar, parity, kWaitNs, abort_flag))) {
-            raise_wait(abort_flag, 2);
+          if (!__all_sync(~0u, wait_working(bar, parity, flags))) {
+            raise_wait(flags, 2);
             failed = true;
           }
           return !failed;
@@ -606,6 +634,7 @@ __global__ void __launch_bounds__(kTThreads, 1) prefill_kernel(const __grid_cons
             release(kt);
             if (t.most == 1 && leader) ptx::umma_commit(q_empty);
             for (int j = 0; j < t.most && !failed; ++j) {
+              if (leader && j % kNote == kNote - 1) note_work(flags);
               if (leader && j + kSoon + 1 == t.most) ptx::mbar_arrive(soon);
               if (!take(vt)) break;
               bool have_k = false;
@@ -637,6 +666,7 @@ __global__ void __launch_bounds__(kTThreads, 1) prefill_kernel(const __grid_cons
             }
             if (t.most <= 2 && leader) ptx::umma_commit(q_empty);
             for (int j = 0; j < t.most && !failed; ++j) {
+              if (leader && j % kNote == kNote - 1) note_work(flags);
               if (leader && j + kSoon + 1 == t.most) ptx::mbar_arrive(soon);
               const int slot = (g + j) & 1;
               if (!take(vt)) break;
@@ -690,7 +720,7 @@ __global__ void __launch_bounds__(kTThreads, 1) prefill_kernel(const __grid_cons
         for (int j = 0; j < nt; ++j) {
           const int slot = NQ == 2 ? sub : (steps + j) & 1;
           const uint32_t s_at = tmem + 128u * slot + lanes;
-          ok = ptx::wait_bounded(s_full + 8u * slot, (NQ == 2 ? steps + j : (steps + j) >> 1) & 1u, kWaitNs, abort_flag);
+          ok = wait_working(s_full + 8u * slot, (NQ == 2 ? steps + j : (steps + j) >> 1) & 1u, flags);
           ok = __all_sync(~0u, ok);
           if (!ok) break;
           ptx::tc_fence_after();
@@ -723,7 +753,7 @@ __global__ void __launch_bounds__(kTThreads, 1) prefill_kernel(const __grid_cons
             const float mn = grows ? top : m;
             if (j > 0) {
               const float f = grows ? exp2_fast(m - mn) : 1.0f;
-              ok = ptx::wait_bounded(pv_done + 8u * sub, (steps + j - 1u) & 1u, kWaitNs, abort_flag);
+              ok = wait_working(pv_done + 8u * sub, (steps + j - 1u) & 1u, flags);
               ok = __all_sync(~0u, ok);
               if (!ok) break;
               ptx::tc_fence_after();
@@ -769,11 +799,11 @@ __global__ void __launch_bounds__(kTThreads, 1) prefill_kernel(const __grid_cons
         }
         steps += nt;
         if (ok && nt > 0) {
-          ok = ptx::wait_bounded(pv_done + 8u * sub, (steps - 1u) & 1u, kWaitNs, abort_flag);
+          ok = wait_working(pv_done + 8u * sub, (steps - 1u) & 1u, flags);
           ok = __all_sync(~0u, ok);
         }
         if (!ok) {
-          if (lane == 0) raise_wait(abort_flag, 3);
+          if (lane == 0) raise_wait(flags, 3);
           break;
         }
         ptx::tc_fence_after();
@@ -834,7 +864,7 @@ __global__ void __launch_bounds__(kTThreads, 1) prefill_kernel(const __grid_cons
           row_by_loops<T, D>(static_cast<const uint16_t*>(a.q) + (t.at.q0 + tr) * a.q_token + hh * a.q_head, k, a.k_token, v,
                              a.v_token, min(max(tr + shift + 1, 0), t.at.k_len), c,
                              static_cast<uint16_t*>(a.out) + (t.at.q0 + tr) * a.out_token + hh * a.out_head,
-                             a.lse ? a.lse + static_cast<int64_t>(hh) * a.total_q + t.at.q0 + tr : nullptr);
+                             a.lse ? a.lse + static_cast<int64_t>(hh) * a.total_q + t.at.q0 + tr : nullptr, flags);
         }
       }
     }

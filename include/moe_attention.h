@@ -62,7 +62,8 @@ moe_status moe_attn_prefill(const moe_attn_prefill_args* args, void* stream);
 
 /*
  * Waits for `stream`, then reports and clears the device's error word of moe_attn_prefill: MOE_ERR_DEVICE_TIMEOUT when a
- * wait inside a kernel since the last check gave up (after 2 s; the outputs it was for are then undefined), else MOE_OK.
+ * wait inside a kernel since the last check gave up (nothing of its CTA had advanced for 2 s; the outputs it was for are
+ * then undefined), else MOE_OK.
  */
 moe_status moe_attn_check(void* stream);
 

@@ -36,3 +36,20 @@ def test_prefill_without_any_keys(d, dtype):
     attention.prefill(q, none, none, kv.ints([0, 30, 30, 70]), kv.ints([0, 0, 0, 0]), out=out, lse=lse)
     attention.raise_on_device_error()
     assert not out.any() and (lse == -math.inf).all()
+
+
+def test_prefill_tiles_that_take_seconds():
+    """2^29 keys, rows 16 bytes apart in one buffer: the only tile takes several seconds, in which most of the kernel's
+    roles wait. One key near the end takes all the weight (the others score 200 nats less)."""
+    from expert_major_chunked_gb300 import attention
+    n, d, key = 1 << 29, 64, (1 << 29) - 6
+    x = torch.zeros(8 * n + 3 * d, dtype=torch.bfloat16, device="cuda")
+    k, v = x.as_strided((n, 1, d), (8, d, 1)), x.as_strided((n, 1, d), (8, d, 1), 2 * d)
+    x[8 * key] = 200.0                       # dimension 0 of this key only
+    q = torch.zeros(1, 1, d, dtype=torch.bfloat16, device="cuda")
+    q[..., 0] = 1.0
+    v[key] = torch.arange(d, device="cuda")  # (it lies past the end of the keys' 64 values)
+    assert k[key + 1:, 0, 0].abs().max() <= d and k[key, 0, 0] == 200
+    out, lse = attention.prefill(q, k, v, kv.ints([0, 1]), kv.ints([0, n]), scale=1.0)
+    attention.raise_on_device_error()
+    assert torch.equal(out[0, 0], v[key, 0]) and abs(lse.item() - 200.0) < 1e-3
