@@ -45,6 +45,7 @@ __device__ __forceinline__ void note_work(volatile Flags* f) { f->worked = ptx::
 
 // A tile of work: `tokens` tokens of a sequence from tok0 on, for a slice of the query heads of a kv head.
 struct TileAt {
+  uint32_t index;  // of the CTA whose tile it is
   int valid, q0, q_len, k0, k_len, tok0, kvh, slice;
 };
 
@@ -125,6 +126,7 @@ struct TileOrder {
         if (lane == 0 && (b0 / 32) % kNote == kNote - 1) note_work(flags);
       }
     }
+    t.index = index;
     t.valid = 1;
     t.kvh = unit / slices;
     t.slice = unit % slices;
@@ -133,49 +135,236 @@ struct TileOrder {
   }
 };
 
-// One row by plain loops that touch only the keys it sees: for rows whose matrix-product result is not finite, where a
-// hidden key or value that is NaN or infinite may have been multiplied by a probability of zero. One warp.
+// ------------------------------------------------------------------ rows whose product is not finite
+// A hidden value that is NaN or infinite, in the last tiles of keys that a tile of rows reads, meets a probability of
+// zero there and makes the row's product NaN. Such rows are noted, and computed again when the CTA is done with its tiles:
+// that function called between the tiles costs the kernel registers, and spills in every step (3001 tokens 59.5 us
+// against 53.5), whether or not there are such rows.
+struct BadRows {
+  uint32_t index, rows;  // of the tile; a bit for each of the warp's 32 rows
+};
+// A warp's list has room for the tiles that are under way when the CTA stops to take further ones (those that have not
+// started then start as CTAs of their own).
+constexpr int kBadRoom = 8, kBadStop = kBadRoom - 2;
+
+// A warp's 32 rows: row0 .. of the 128 of a sub-tile; row r is token first_tok + r / hpt and head head0 + r % hpt, for
+// n_tok tokens and `heads` heads.
+struct RowsAt {
+  int q0, k0, shift, head0, kvh, first_tok, n_tok, hpt, heads, row0;
+};
+
+// The first and the last of the keys `from` .. `to` - 1 whose value has a NaN or an infinity (2^31 - 1, -1: none). One warp;
+// with `any`, it stops at the first ones that it meets.
 template <class T, int D>
-__device__ __noinline__ void row_by_loops(const uint16_t* q, const uint16_t* k, int64_t k_token, const uint16_t* v,
-                                          int64_t v_token, int keys, float c, uint16_t* out, float* lse,
-                                          volatile Flags* flags) {
-  constexpr int W = D / 64;
+__device__ int2 unfinite_keys(const uint16_t* v, int64_t v_token, int from, int to, bool any, volatile Flags* flags) {
+  constexpr int CHUNKS = D / 8, KEYS = 32 / CHUNKS, AHEAD = 8;  // 16 bytes a lane, KEYS keys a pass
+  constexpr uint32_t E = T::kCode == 0 ? 0x7F80u : 0x7C00u;     // the exponent's bits
   const int lane = threadIdx.x & 31;
-  float2 qf[W], o[W];
-  float m = -INFINITY, l = 0.0f;
+  int2 at = make_int2(0x7FFFFFFF, -1);
+  for (int j = from; j < to; j += KEYS * AHEAD) {
+    uint4 x[AHEAD];
 #pragma unroll
-  for (int i = 0; i < W; ++i) {
-    qf[i] = T::unpack(*reinterpret_cast<const uint32_t*>(q + 2 * (lane + 32 * i)));
-    o[i] = make_float2(0.0f, 0.0f);
-  }
-  for (int j = 0; j < keys; ++j) {
-    float s = 0.0f;
-#pragma unroll
-    for (int i = 0; i < W; ++i) {
-      const float2 kf = T::unpack(*reinterpret_cast<const uint32_t*>(k + j * k_token + 2 * (lane + 32 * i)));
-      s = fmaf(qf[i].x, kf.x, fmaf(qf[i].y, kf.y, s));
+    for (int i = 0; i < AHEAD; ++i) {
+      const int key = j + i * KEYS + lane / CHUNKS;
+      x[i] = key < to ? *reinterpret_cast<const uint4*>(v + key * v_token + lane % CHUNKS * 8) : make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
-    for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(~0u, s, d);
-    s *= c;
-    if (lane == 0 && j % kNote == kNote - 1) note_work(flags);
-    const float mn = s > m || !(s == s) ? s : m;  // a NaN score makes the row NaN
-    const float ms = mn == -INFINITY ? 0.0f : mn;
-    const float f = exp2_fast(m - ms), p = exp2_fast(s - ms);
-    l = l * f + p;
+    for (int i = 0; i < AHEAD; ++i) {
+      const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+      bool hit = false;
 #pragma unroll
-    for (int i = 0; i < W; ++i) {
-      const float2 vf = T::unpack(*reinterpret_cast<const uint32_t*>(v + j * v_token + 2 * (lane + 32 * i)));
-      o[i].x = o[i].x * f + p * vf.x;
-      o[i].y = o[i].y * f + p * vf.y;
+      for (int k = 0; k < 4; ++k) hit |= (w[k] & E) == E || (w[k] >> 16 & E) == E;
+      const int key = j + i * KEYS + lane / CHUNKS;
+      if (hit) at = make_int2(min(at.x, key), key);
     }
-    m = mn;
+    if (any && __any_sync(~0u, at.y >= 0)) break;
+    if (lane == 0 && (j - from) / (KEYS * AHEAD) % kNote == kNote - 1) note_work(flags);
   }
-  const float inv = l > 0.0f ? 1.0f / l : (l == l ? 0.0f : l);
+  return make_int2(__reduce_min_sync(~0u, at.x), __reduce_max_sync(~0u, at.y));
+}
+
+// 16 rows (r0 .. of the 128) again, those of `which` written: 16 keys at a time as warp-level matrix products as long as
+// every row sees them, then key by key for the rows that see it. A pass makes up to 128 dims of the output (all 256 would
+// take more registers than there are).
+template <class T, int D>
+__device__ __noinline__ void rows_again(const moe_attn_prefill_args& a, const RowsAt& at, int r0, uint32_t which,
+                                        float c) {
+  constexpr float top = T::kCode == 1 ? 15.0f : 0.0f;  // log2 of the largest weight
+  constexpr int CH = D < 128 ? D : 128;
+  const int lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
+  const uint16_t* k = static_cast<const uint16_t*>(a.k) + at.k0 * a.k_token + at.kvh * a.k_head;
+  const uint16_t* v = static_cast<const uint16_t*>(a.v) + at.k0 * a.v_token + at.kvh * a.v_head;
+  const uint16_t* q[2];  // this lane's rows: r0 + g and r0 + g + 8
+  int64_t tok[2];
+  int head[2], lim[2];
 #pragma unroll
-  for (int i = 0; i < W; ++i)
-    *reinterpret_cast<uint32_t*>(out + 2 * (lane + 32 * i)) = T::pack(o[i].x * inv, o[i].y * inv);
-  if (lse && lane == 0) *lse = l == 0.0f ? -INFINITY : (m + log2_fast(l)) * kLn2;
+  for (int e = 0; e < 2; ++e) {
+    const int r = r0 + g + 8 * e, row_tok = r / at.hpt, row_head = r % at.hpt;
+    const bool real = row_tok < at.n_tok && row_head < at.heads;
+    tok[e] = at.q0 + at.first_tok + row_tok, head[e] = at.head0 + row_head;
+    lim[e] = real ? at.first_tok + row_tok + at.shift : -1;
+    q[e] = real ? static_cast<const uint16_t*>(a.q) + tok[e] * a.q_token + head[e] * a.q_head : nullptr;
+  }
+  const int all_see = at.first_tok + r0 / at.hpt + at.shift + 1;  // keys that every row sees: the first row's
+  const int blocks = max(all_see, 0) / 16, last = __reduce_max_sync(~0u, max(lim[0], lim[1]));
+  auto load = [](const uint16_t* p) { return p ? *reinterpret_cast<const uint4*>(p) : make_uint4(0, 0, 0, 0); };
+
+#pragma unroll 1
+  for (int d0 = 0; d0 < D; d0 += CH) {
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+    // Loads are 16 bytes a lane. Of 32 dims of Q and K a lane has 8 t4 .. + 7, four of them for each of two products (their
+    // order does not matter as long as it is the same). Of 64 dims of V it has 8 g .. + 7, one for each of eight products: the
+    // results are dims 16 t4 + i (o[..][i][0] and [2] for the second row) and 16 t4 + 8 + i ([1] and [3]).
+    float o[CH / 64][8][4];
+#pragma unroll
+    for (int j = 0; j < CH / 64; ++j)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[j][i][0] = o[j][i][1] = o[j][i][2] = o[j][i][3] = 0.0f;
+    auto scale_rows = [&](float f0, float f1) {
+      l[0] *= f0, l[1] *= f1;
+#pragma unroll
+      for (int j = 0; j < CH / 64; ++j)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[j][i][0] *= f0, o[j][i][1] *= f0, o[j][i][2] *= f1, o[j][i][3] *= f1;
+    };
+
+    for (int b = 0; b < blocks; ++b) {
+      const uint16_t* kb = k + static_cast<int64_t>(b * 16 + g) * a.k_token + 8 * t4;
+      const uint16_t* vb = v + static_cast<int64_t>(b * 16 + 2 * t4) * a.v_token + d0 + 8 * g;
+      float s[2][4] = {};
+#pragma unroll 4
+      for (int kk = 0; kk < D; kk += 32) {
+        const uint4 q0 = load(q[0] ? q[0] + kk + 8 * t4 : nullptr), q1 = load(q[1] ? q[1] + kk + 8 * t4 : nullptr);
+        const uint32_t a0[4] = {q0.x, q1.x, q0.y, q1.y}, a1[4] = {q0.z, q1.z, q0.w, q1.w};
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          const uint4 kw = load(kb + 8 * n * a.k_token + kk);
+          mma_16816<T>(s[n], a0, kw.x, kw.y);
+          mma_16816<T>(s[n], a1, kw.z, kw.w);
+        }
+      }
+      float f[2], ms[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float x = fmaxf(fmaxf(s[0][2 * e], s[0][2 * e + 1]), fmaxf(s[1][2 * e], s[1][2 * e + 1]));
+        x = fmaxf(x, __shfl_xor_sync(~0u, x, 1));
+        x = fmaxf(x, __shfl_xor_sync(~0u, x, 2)) * c;
+        const float mn = x > m[e] ? x : m[e];
+        ms[e] = mn == -INFINITY ? 0.0f : mn;
+        f[e] = exp2_fast(m[e] - ms[e]);
+        m[e] = mn;
+      }
+      if (__any_sync(~0u, f[0] != 1.0f || f[1] != 1.0f)) scale_rows(f[0], f[1]);
+      uint32_t p[4];
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float x = exp2_fast(fmaf(s[n][2 * e], c, top - ms[e])), y = exp2_fast(fmaf(s[n][2 * e + 1], c, top - ms[e]));
+          l[e] += x + y;
+          p[2 * n + e] = T::pack(x, y);
+        }
+#pragma unroll
+      for (int j = 0; j < CH / 64; ++j) {
+        const uint4 w0 = load(vb + 64 * j), w1 = load(vb + 64 * j + a.v_token);
+        const uint4 w2 = load(vb + 64 * j + 8 * a.v_token), w3 = load(vb + 64 * j + 9 * a.v_token);
+        const uint32_t x[4][4] = {{w0.x, w1.x, w2.x, w3.x}, {w0.y, w1.y, w2.y, w3.y}, {w0.z, w1.z, w2.z, w3.z},
+                                  {w0.w, w1.w, w2.w, w3.w}};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint32_t half = i & 1 ? 0x7632 : 0x5410, *w = x[i / 2];
+          mma_16816<T>(o[j][i], p, __byte_perm(w[0], w[1], half), __byte_perm(w[2], w[3], half));
+        }
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      l[e] += __shfl_xor_sync(~0u, l[e], 1);
+      l[e] += __shfl_xor_sync(~0u, l[e], 2);
+    }
+    for (int key = blocks * 16; key <= last; ++key) {
+      const uint16_t *kr = k + key * a.k_token + 8 * t4, *vr = v + key * a.v_token + d0 + 16 * t4;
+      float s[2] = {0.0f, 0.0f};
+#pragma unroll 1
+      for (int j = 0; j < D; j += 32) {
+        const uint4 kw = load(kr + j);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const uint4 qw = load(q[e] ? q[e] + j + 8 * t4 : nullptr);
+          const uint32_t x[4] = {qw.x, qw.y, qw.z, qw.w}, y[4] = {kw.x, kw.y, kw.z, kw.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 xf = T::unpack(x[i]), yf = T::unpack(y[i]);
+            s[e] = fmaf(xf.x, yf.x, fmaf(xf.y, yf.y, s[e]));
+          }
+        }
+      }
+      float f[2], p[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        s[e] += __shfl_xor_sync(~0u, s[e], 1);
+        s[e] += __shfl_xor_sync(~0u, s[e], 2);
+        const bool sees = key <= lim[e];
+        const float x = s[e] * c, mn = sees && x > m[e] ? x : m[e], ms = mn == -INFINITY ? 0.0f : mn;
+        f[e] = exp2_fast(m[e] - ms);
+        p[e] = sees ? exp2_fast(x - ms + top) : 0.0f;
+        m[e] = mn;
+      }
+      scale_rows(f[0], f[1]);
+      l[0] += p[0], l[1] += p[1];
+#pragma unroll
+      for (int j = 0; j < CH / 64; ++j)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const uint4 vw = load(vr + 64 * j + 8 * half);
+          const uint32_t w[4] = {vw.x, vw.y, vw.z, vw.w};
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            if (key > lim[e]) continue;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float2 x = T::unpack(w[i]);
+              o[j][2 * i][2 * e + half] = fmaf(p[e], x.x, o[j][2 * i][2 * e + half]);
+              o[j][2 * i + 1][2 * e + half] = fmaf(p[e], x.y, o[j][2 * i + 1][2 * e + half]);
+            }
+          }
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      if (!(which >> (g + 8 * e) & 1u)) continue;
+      const float il = l[e] == 0.0f ? 0.0f : 1.0f / l[e];
+      uint16_t* out = static_cast<uint16_t*>(a.out) + tok[e] * a.out_token + head[e] * a.out_head + d0 + 16 * t4;
+#pragma unroll
+      for (int j = 0; j < CH / 64; ++j)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t w[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            w[i] = T::pack(o[j][2 * i][2 * e + half] * il, o[j][2 * i + 1][2 * e + half] * il);
+          *reinterpret_cast<uint4*>(out + 64 * j + 8 * half) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      if (a.lse && t4 == 0 && d0 == 0)
+        a.lse[static_cast<int64_t>(head[e]) * a.total_q + tok[e]] =
+            l[e] == 0.0f ? -INFINITY : (m[e] - top + log2_fast(l[e])) * kLn2;
+    }
+  }
+}
+
+// Which of the rows of `which` (a bit a lane, whose row sees keys up to `lim` of v) are to be computed again; their product
+// is not finite although their sum is. A row stays as it is where it sees a value that is not finite, unless its tiles of
+// `keys` keys have a hidden one as well. (Where there is none at all the sums have overflowed: weights are up to 2^8 there,
+// and up to 1 when the row is computed again.)
+template <class T, int D>
+__device__ __noinline__ uint32_t rows_to_mend(const uint16_t* v, int64_t v_token, int lim, int keys, uint32_t which,
+                                              volatile Flags* flags) {
+  const int lane = threadIdx.x & 31, all_see = min(max(__shfl_sync(~0u, lim, 0) + 1, 0), keys);
+  const int2 late = unfinite_keys<T, D>(v, v_token, all_see, keys, false, flags);
+  const bool mine = which >> lane & 1u, hidden = mine && late.y > lim, unclear = mine && !hidden && late.x > lim;
+  bool again = hidden;
+  if (__any_sync(~0u, unclear) && unfinite_keys<T, D>(v, v_token, 0, all_see, true, flags).y < 0) again |= unclear;
+  return __ballot_sync(~0u, again);
 }
 
 // ------------------------------------------------------------------ tcgen05 tiles
@@ -216,7 +405,7 @@ struct Tc {
   static constexpr int VKEYS = kTKeys / PARTS;         // keys of a stage of values
   static constexpr int READERS = 4 * NQ + 3;           // warps that read a tile's record
   static constexpr int QBYTES = NQ * kTRows * D * 2;
-  static constexpr int SMEM = 1024 + QBYTES + STAGES * STAGE + 512;
+  static constexpr int SMEM = 1024 + QBYTES + STAGES * STAGE + 1056;
   static_assert(SMEM <= 232448, "shared memory per CTA");
 };
 
@@ -340,8 +529,30 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 }
 
 __device__ __forceinline__ void write_record(volatile TileAt& r, const TileAt& t) {
-  r.valid = t.valid, r.q0 = t.q0, r.q_len = t.q_len, r.k0 = t.k0, r.k_len = t.k_len;
+  r.index = t.index, r.valid = t.valid, r.q0 = t.q0, r.q_len = t.q_len, r.k0 = t.k0, r.k_len = t.k_len;
   r.tok0 = t.tok0, r.kvh = t.kvh, r.slice = t.slice;
+}
+
+// The rows that a softmax warp has noted. 16022 tokens, 16 heads on 2 of 128, with a NaN behind the last: 3.4 ms a call
+// against 0.54 without (4.6 with loads of 4 bytes a lane; row after row and key after key 138).
+template <class T, int D>
+__device__ void mend_rows(const TcParams& p, const volatile BadRows* list, int n, volatile Flags* flags) {
+  constexpr int NQ = Tc<D>::NQ;
+  const moe_attn_prefill_args& a = p.a;
+  const int group = a.n_heads / a.n_kv_heads, hpt = p.heads_per_tile, sub_tokens = kTRows / hpt;
+  const int warp = threadIdx.x >> 5, sub = NQ == 2 ? warp >> 2 : 0;
+  if (n == 0) return;
+  const TileOrder order(a, flags, NQ * sub_tokens, p.slices);
+  for (int i = 0; i < n; ++i) {
+    TileAt t{};
+    if (!order.find(list[i].index, t)) return;
+    const int first_tok = t.tok0 + sub * sub_tokens;
+    const RowsAt at = {t.q0, t.k0, t.k_len - t.q_len, t.kvh * group + t.slice * hpt, t.kvh, first_tok,
+                       max(0, min(sub_tokens, t.q_len - first_tok)), hpt, min(hpt, group - t.slice * hpt), (warp & 3) * 32};
+    for (int half = 0; half < 2; ++half)
+      if (const uint32_t rows = list[i].rows >> (16 * half) & 0xFFFFu)
+        rows_again<T, D>(a, at, at.row0 + 16 * half, rows, a.scale * kLog2e);
+  }
 }
 
 template <class T, int D>
@@ -363,6 +574,9 @@ __global__ void __launch_bounds__(kTThreads, 1) prefill_kernel(const __grid_cons
   volatile TileAt* records = reinterpret_cast<volatile TileAt*>(tail + sizeof(Flags));  // [2]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tail + sizeof(Flags) + 2 * sizeof(TileAt));
   static_assert(8 * (2 * C::STAGES + 17) + sizeof(Flags) + 2 * sizeof(TileAt) + 4 <= 448, "barriers and records");
+  volatile BadRows* bad_rows = reinterpret_cast<volatile BadRows*>(smem_raw + (bars + 512u - raw));  // [8][kBadRoom]
+  volatile int* n_bad = reinterpret_cast<volatile int*>(bad_rows + 8 * kBadRoom);                    // [8]
+  static_assert(512 + 8 * kBadRoom * sizeof(BadRows) + 8 * sizeof(int) <= 1056, "lists of rows");
   const int warp = __shfl_sync(~0u, static_cast<int>(threadIdx.x) >> 5, 0), lane = static_cast<int>(threadIdx.x) & 31;
   const int group = a.n_heads / a.n_kv_heads, hpt = p.heads_per_tile, sub_tokens = kTRows / hpt;
 
@@ -392,6 +606,7 @@ __global__ void __launch_bounds__(kTThreads, 1) prefill_kernel(const __grid_cons
     ptx::mbar_init(taken, 1);
     ptx::mbar_init(soon, 1);
     flags->abort = 0;
+    for (int w = 0; w < 8; ++w) n_bad[w] = 0;
     ptx::fence_barrier_init();
   }
   if (warp == 8 && lane == 0 && a.total_k > 0) {  // (without keys there are no such maps)
@@ -421,7 +636,7 @@ __global__ void __launch_bounds__(kTThreads, 1) prefill_kernel(const __grid_cons
       return false;
     }
     const volatile TileAt& r = records[it & 1];
-    t.at.valid = r.valid, t.at.q0 = r.q0, t.at.q_len = r.q_len, t.at.k0 = r.k0, t.at.k_len = r.k_len;
+    t.at.index = r.index, t.at.valid = r.valid, t.at.q0 = r.q0, t.at.q_len = r.q_len, t.at.k0 = r.k0, t.at.k_len = r.k_len;
     t.at.tok0 = r.tok0, t.at.kvh = r.kvh, t.at.slice = r.slice;
     t.most = 0;
 #pragma unroll
@@ -531,8 +746,12 @@ __global__ void __launch_bounds__(kTThreads, 1) prefill_kernel(const __grid_cons
       };
       bool have = records[0].valid != 0, ok = true;
       for (int it = 1; have; ++it) {
-        ok = __all_sync(~0u, wait_working(rec_empty + 8u * (it & 1), ((it >> 1) & 1) ^ 1, flags)) &&
-             __all_sync(~0u, wait_working(soon, (it - 1) & 1, flags)) && ask();
+        ok = __all_sync(~0u, wait_working(rec_empty + 8u * (it & 1), ((it >> 1) & 1) ^ 1, flags));
+        // (the lists are those of tiles up to it - 3: it - 2, it - 1 and this one may add to them)
+        if (__any_sync(~0u, n_bad[lane & 7] >= kBadStop))
+          more = false;
+        else
+          ok = ok && __all_sync(~0u, wait_working(soon, (it - 1) & 1, flags)) && ask();
         if (!ok) {
           if (lane == 0) raise_wait(flags, 6);
           break;
@@ -807,8 +1026,7 @@ __global__ void __launch_bounds__(kTThreads, 1) prefill_kernel(const __grid_cons
           break;
         }
         ptx::tc_fence_after();
-        bool bad = !finite_bits(l) || (m != -INFINITY && !finite_bits(m));
-        const float il = l > 0.0f ? 1.0f / l : 0.0f;
+        const float il = l == 0.0f ? 0.0f : 1.0f / l;  // (NaN from a score that the row sees makes all of it NaN)
         // A row a thread would store 16 bytes of 32 rows at a time: four neighbours exchange their 16-byte pieces first, and
         // then store 64 bytes of 8 rows. Offsets of the four rows, -1 for one that is not there:
         const int64_t own = real ? (t.at.q0 + tok) * a.out_token + h * a.out_head : -1;
@@ -847,26 +1065,24 @@ __global__ void __launch_bounds__(kTThreads, 1) prefill_kernel(const __grid_cons
               *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + row_at[k] + i + (lane & 3) * 8) =
                   make_uint4(w[k][0], w[k][1], w[k][2], w[k][3]);
         }
-        bad |= !(zero.x == 0.0f && zero.y == 0.0f);
+        const bool bad = real && finite_bits(l) && !(zero.x == 0.0f && zero.y == 0.0f);
         ptx::tc_fence_before();
         if (real && a.lse)
           a.lse[static_cast<int64_t>(h) * a.total_q + t.at.q0 + tok] =
-              l > 0.0f ? (m - kTop<T> + log2_fast(l)) * kLn2 : -INFINITY;
-        uint32_t again = __ballot_sync(~0u, bad && real);
-        const uint16_t* k = static_cast<const uint16_t*>(a.k) + t.at.k0 * a.k_token + t.at.kvh * a.k_head;
-        const uint16_t* v = static_cast<const uint16_t*>(a.v) + t.at.k0 * a.v_token + t.at.kvh * a.v_head;
-        while (again) {
-          const int src = __ffs(again) - 1;
-          again &= again - 1;
-          const int r = (warp & 3) * 32 + src, tr = first_tok + r / hpt;
-          const int hh = t.at.kvh * group + t.at.slice * hpt + r % hpt;
-          __syncwarp();
-          row_by_loops<T, D>(static_cast<const uint16_t*>(a.q) + (t.at.q0 + tr) * a.q_token + hh * a.q_head, k, a.k_token, v,
-                             a.v_token, min(max(tr + shift + 1, 0), t.at.k_len), c,
-                             static_cast<uint16_t*>(a.out) + (t.at.q0 + tr) * a.out_token + hh * a.out_head,
-                             a.lse ? a.lse + static_cast<int64_t>(hh) * a.total_q + t.at.q0 + tr : nullptr, flags);
+              l == 0.0f ? -INFINITY : (m - kTop<T> + log2_fast(l)) * kLn2;
+        if (const uint32_t which = __ballot_sync(~0u, bad)) {
+          const uint16_t* v = static_cast<const uint16_t*>(a.v) + t.at.k0 * a.v_token + t.at.kvh * a.v_head;
+          const uint32_t rows = rows_to_mend<T, D>(v, a.v_token, lim, min(nt * kTKeys, a.total_k - t.at.k0), which, flags);
+          if (rows && lane == 0) {
+            const int n = n_bad[warp];
+            bad_rows[warp * kBadRoom + n].index = t.at.index;
+            bad_rows[warp * kBadRoom + n].rows = rows;
+            n_bad[warp] = n + 1;
+          }
         }
       }
+      __syncwarp();
+      mend_rows<T, D>(p, bad_rows + warp * kBadRoom, n_bad[warp], flags);
     }
   }
   ptx::tc_fence_before();

@@ -41,7 +41,10 @@ enum { MOE_ATTN_BF16 = 0, MOE_ATTN_F16 = 1 };
  * query that sees no key (k_len < q_len) gets zeros and lse = -inf. Rows of out and lse that belong to no sequence (from
  * cu_q[n_seqs] on) are not written.
  *   out[t][h] = sum_j softmax_j(scale * q[t][h] . k[j][h']) v[j][h'],   lse[h][t] = ln sum_j exp(scale * q . k_j)
- * A row's output does not depend on how the prompt is cut into chunks, nor on the other sequences of the call.
+ * A row's output does not depend on how the prompt is cut into chunks, nor on the other sequences of the call, to the last
+ * bit as long as the values are finite. Where a value that it does not see is not, a row may be computed another way,
+ * which moves its last bits. A channel in which a row sees a NaN or an infinity is not finite. out must not overlap the
+ * inputs.
  * Limits: n_seqs, total_q and total_k up to 2^30, (total_q + n_seqs) * n_heads below 2^31. Rows of q, k, v and out must
  * be apart (strides above 0); the head stride of k and v may be 0, one head's rows for all.
  */
