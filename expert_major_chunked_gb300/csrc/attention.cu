@@ -50,12 +50,13 @@ bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p
 
 moe_status check_device() noexcept {
   // the answer for a device does not change, so it is looked up once for each
-  static int major[64], minor[64];
-  static bool known[64];
+  static int major[kMaxDevices], minor[kMaxDevices];
+  static bool known[kMaxDevices];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "cudaGetDevice: %s", cudaGetErrorString(e));
-  if (dev < 0 || dev >= 64) return fail(MOE_ERR_UNSUPPORTED, "device %d: only 0..63 are supported", dev);
+  if (dev < 0 || dev >= kMaxDevices)
+    return fail(MOE_ERR_UNSUPPORTED, "device %d: only 0..%d are supported", dev, kMaxDevices - 1);
   if (!__atomic_load_n(&known[dev], __ATOMIC_ACQUIRE)) {
     int ma = 0, mi = 0;
     e = cudaDeviceGetAttribute(&ma, cudaDevAttrComputeCapabilityMajor, dev);

@@ -3,6 +3,7 @@
 #pragma once
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include <atomic>
 #include <cstdint>
 
 #include "../../include/moe_attention.h"
@@ -19,6 +20,28 @@ cudaError_t launch_attn_decode(const moe_attn_decode_args& a, cudaStream_t strea
 
 // Waits for the stream, reads moe_attn_prefill's error word and clears it (0: no wait in the kernel gave up).
 cudaError_t attn_prefill_take_error(int* site, cudaStream_t stream);
+
+constexpr int kMaxDevices = 64;  // ordinals that the C entries take
+
+// What has to be done once on each device, such as a kernel's attributes; an attempt that fails is made again. (Threads
+// that come first together may both do it.)
+class OncePerDevice {
+ public:
+  template <class F>
+  cudaError_t operator()(F prepare) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    if (done_[dev].load(std::memory_order_acquire)) return cudaSuccess;
+    e = prepare();
+    if (e == cudaSuccess) done_[dev].store(true, std::memory_order_release);
+    return e;
+  }
+
+ private:
+  std::atomic<bool> done_[kMaxDevices] = {};
+};
 
 // Launches a kernel whose set-up may run beside the end of the work before it in the stream: the kernel waits for that
 // work (griddepcontrol.wait) before it touches global memory. Back to back, a call of a few microseconds otherwise takes

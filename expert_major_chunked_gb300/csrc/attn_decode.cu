@@ -24,7 +24,6 @@
 #include "attn.cuh"
 
 #include <algorithm>
-#include <mutex>
 
 namespace moe {
 namespace {
@@ -557,16 +556,14 @@ template <class T, int D, int NH>
 cudaError_t launch_decode(const moe_attn_decode_args& a, cudaStream_t stream) {
   constexpr int ring = kDecWarps * kDecStages * kStageBytes, join = kDecWarps * 8 * NH * (D + 4) * 4;
   constexpr int smem = ring > join ? ring : join;
-  static std::once_flag once;  // function attributes are kept for every device
-  static cudaError_t prepared;
-  std::call_once(once, [] {
-    prepared = cudaFuncSetAttribute(decode_kernel<T, D, NH>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static OncePerDevice prepared;
+  cudaError_t e = prepared([] {
+    return cudaFuncSetAttribute(decode_kernel<T, D, NH>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   });
-  if (prepared != cudaSuccess) return prepared;
+  if (e != cudaSuccess) return e;
   int block_log2 = 0;
   while ((1 << block_log2) < a.block_size) ++block_log2;
-  const cudaError_t e =
-      launch_early(decode_kernel<T, D, NH>, dim3(kDecCtas), dim3(kDecThreads), smem, stream, a, block_log2);
+  e = launch_early(decode_kernel<T, D, NH>, dim3(kDecCtas), dim3(kDecThreads), smem, stream, a, block_log2);
   if (e != cudaSuccess) return e;
   const DecodeGeom geo = decode_geom(a.n_heads, a.n_kv_heads);
   const int64_t units = static_cast<int64_t>(geo.units_per_tile) * a.n_requests;

@@ -17,7 +17,6 @@
 #include "attn.cuh"
 
 #include <algorithm>
-#include <mutex>
 
 namespace moe {
 namespace {
@@ -1131,12 +1130,11 @@ bool encode_queries(CUtensorMap* m, const moe_attn_prefill_args& a, int heads, i
 template <class T, int D>
 cudaError_t launch_tiles(const moe_attn_prefill_args& a, cudaStream_t stream) {
   using C = Tc<D>;
-  static std::once_flag once;  // function attributes are kept for every device
-  static cudaError_t prepared;
-  std::call_once(once, [] {
-    prepared = cudaFuncSetAttribute(prefill_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  static OncePerDevice prepared;
+  const cudaError_t e = prepared([] {
+    return cudaFuncSetAttribute(prefill_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   });
-  if (prepared != cudaSuccess) return prepared;
+  if (e != cudaSuccess) return e;
   TcParams p;
   p.a = a;
   const int group = a.n_heads / a.n_kv_heads;
