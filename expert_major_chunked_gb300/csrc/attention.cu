@@ -48,20 +48,27 @@ constexpr int32_t kPrefillMax = 1 << 30;  // row numbers and tile numbers stay w
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
+moe_status cuda_failed(cudaError_t e, const char* what) noexcept {
+  cudaGetLastError();  // reported here, so not left for another call of the thread to find
+  return fail(MOE_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+}
+
+moe_status launched(cudaError_t e, const char* what) noexcept { return e == cudaSuccess ? MOE_OK : cuda_failed(e, what); }
+
 moe_status check_device() noexcept {
   // the answer for a device does not change, so it is looked up once for each
   static int major[kMaxDevices], minor[kMaxDevices];
   static bool known[kMaxDevices];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "cudaGetDevice: %s", cudaGetErrorString(e));
+  if (e != cudaSuccess) return cuda_failed(e, "cudaGetDevice");
   if (dev < 0 || dev >= kMaxDevices)
     return fail(MOE_ERR_UNSUPPORTED, "device %d: only 0..%d are supported", dev, kMaxDevices - 1);
   if (!__atomic_load_n(&known[dev], __ATOMIC_ACQUIRE)) {
     int ma = 0, mi = 0;
     e = cudaDeviceGetAttribute(&ma, cudaDevAttrComputeCapabilityMajor, dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&mi, cudaDevAttrComputeCapabilityMinor, dev);
-    if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "cudaDeviceGetAttribute: %s", cudaGetErrorString(e));
+    if (e != cudaSuccess) return cuda_failed(e, "cudaDeviceGetAttribute");
     __atomic_store_n(&major[dev], ma, __ATOMIC_RELAXED);
     __atomic_store_n(&minor[dev], mi, __ATOMIC_RELAXED);
     __atomic_store_n(&known[dev], true, __ATOMIC_RELEASE);
@@ -69,11 +76,6 @@ moe_status check_device() noexcept {
   if (major[dev] != 10 || minor[dev] != 3)
     return fail(MOE_ERR_ARCH, "device %d is sm_%d%d; the kernels are built for sm_103a", dev, major[dev], minor[dev]);
   return MOE_OK;
-}
-
-moe_status launched(cudaError_t e, const char* what) noexcept {
-  if (e == cudaSuccess) return MOE_OK;
-  return fail(MOE_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
 moe_status check_heads(int n_heads, int n_kv_heads, int head_dim, int dtype) noexcept {

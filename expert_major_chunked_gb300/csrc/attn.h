@@ -60,8 +60,7 @@ cudaError_t launch_early(void (*kernel)(P...), dim3 grid, dim3 block, size_t sme
   cfg.stream = stream;
   cfg.attrs = &early;
   cfg.numAttrs = 1;
-  cudaLaunchKernelEx(&cfg, kernel, P(args)...);
-  return cudaGetLastError();
+  return cudaLaunchKernelEx(&cfg, kernel, P(args)...);  // (the runtime's last error may be some earlier call's)
 }
 
 // cuTensorMapEncodeTiled of the driver, or nullptr
