@@ -103,6 +103,14 @@ moe_status check_walk(const char* name, int64_t stride, int64_t count) noexcept 
   return MOE_OK;
 }
 
+// Rows that are written lie apart.
+moe_status check_out(const void* p, int64_t token, int64_t tokens, int64_t head, int64_t heads, int dim) noexcept {
+  const moe_status st = check_rows("out", p, token, head);
+  if (st != MOE_OK) return st;
+  REQUIRE((tokens <= 1 || token >= dim) && (heads <= 1 || head >= dim), "out: rows must be at least head_dim apart");
+  return MOE_OK;
+}
+
 moe_status check_block(int block_size, int num_blocks) noexcept {
   if (block_size != 16 && block_size != 32 && block_size != 64 && block_size != 128)
     return fail(MOE_ERR_UNSUPPORTED, "block_size %d: 16, 32, 64 and 128 are supported", block_size);
@@ -134,7 +142,7 @@ moe_status moe_attn_prefill(const moe_attn_prefill_args* p, void* stream) {
   TRY(check_rows("q", a.q, a.q_token, a.q_head));
   TRY(check_walk("q", a.q_token, a.total_q));
   TRY(check_walk("q", a.q_head, a.n_heads));
-  TRY(check_rows("out", a.out, a.out_token, a.out_head));
+  TRY(check_out(a.out, a.out_token, a.total_q, a.out_head, a.n_heads, a.head_dim));
   if (a.total_k > 0) {
     TRY(check_rows("k", a.k, a.k_token, a.k_head));
     TRY(check_walk("k", a.k_token, a.total_k));
@@ -208,7 +216,7 @@ moe_status moe_attn_decode(const moe_attn_decode_args* p, void* stream) {
   REQUIRE(std::isfinite(a.scale) && a.scale > 0.0f, "scale must be positive and finite");
   if (a.n_requests == 0) return MOE_OK;
   TRY(check_rows("q", a.q, a.q_token, a.q_head));
-  TRY(check_rows("out", a.out, a.out_token, a.out_head));
+  TRY(check_out(a.out, a.out_token, a.n_requests, a.out_head, a.n_heads, a.head_dim));
   REQUIRE(a.kv_lens && aligned(a.kv_lens, 4), "kv_lens must be an int32 array");
   REQUIRE(a.max_blocks == 0 || (a.block_table && aligned(a.block_table, 4) && a.table_stride >= a.max_blocks),
           "block_table must have int32 rows of at least max_blocks entries");

@@ -45,8 +45,9 @@ enum { MOE_ATTN_BF16 = 0, MOE_ATTN_F16 = 1 };
  * bit as long as the values are finite. Where a value that it does not see is not, a row may be computed another way,
  * which moves its last bits. A channel in which a row sees a NaN or an infinity is not finite. out must not overlap the
  * inputs.
- * Limits: n_seqs, total_q and total_k up to 2^30, (total_q + n_seqs) * n_heads below 2^31. Rows of q, k, v and out must
- * be apart (strides above 0); the head stride of k and v may be 0, one head's rows for all.
+ * Limits: n_seqs, total_q and total_k up to 2^30, (total_q + n_seqs) * n_heads below 2^31. Rows of q, k and v must be
+ * apart (strides above 0); the head stride of k and v may be 0, one head's rows for all. Rows of out must be at least
+ * head_dim apart.
  */
 typedef struct {
   const void* q;        /* [total_q][n_heads][head_dim] */
@@ -128,9 +129,9 @@ moe_status moe_kv_append(const moe_kv_append_args* args, void* stream);
 /*
  * Attention of one query token a request over the cache: request b attends to its first kv_lens[b] slots (at most
  * max_blocks * block_size), in the blocks block_table[b][..]; slots whose block id lies outside the cache are left out. No
- * slot: zeros and lse = -inf. Scales may be any normal float32 values from 2^-40 to 2^40; a V scale of 0 leaves its block
- * out. The cache is split over the GPU by the requests' lengths and the pieces are joined in a fixed order: the same call
- * gives the same bytes.
+ * slot: zeros and lse = -inf. Rows of out must be at least head_dim apart. Scales may be any normal float32 values from
+ * 2^-40 to 2^40; a V scale of 0 leaves its block out. The cache is split over the GPU by the requests' lengths and the
+ * pieces are joined in a fixed order: the same call gives the same bytes.
  * workspace: moe_attn_decode_workspace() bytes, 16-byte aligned, needs no initialisation; calls that overlap on the GPU
  * need one each.
  */
