@@ -81,6 +81,10 @@ __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, uint32_
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 
+__device__ __forceinline__ void zero16(uint32_t dst) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(dst), "r"(0) : "memory");
+}
+
 // an 8 x 8 matrix of 16-bit values, two of a row a lane, transposed across the warp
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t y;
@@ -340,6 +344,14 @@ __global__ void __launch_bounds__(kDecThreads, 2) decode_kernel(const __grid_con
           x[n][0] = fmaxf(x[n][0], __shfl_xor_sync(~0u, x[n][0], d));
           x[n][1] = fmaxf(x[n][1], __shfl_xor_sync(~0u, x[n][1], d));
         }
+      if (!full) {  // a block that is left out for its scale: its codes may be NaN, which a weight of 0 does not hide
+#pragma unroll
+        for (int i = 0; i < TT; ++i)
+          if (!(sc_sh[4 + i] > 0.0f))
+            for (int x = lane; x < D; x += 32)
+              zero16(st + kCodeBytes + code_at<D>(i * 16 + x / (D / 16), x % (D / 16)));
+        __syncwarp();
+      }
       bool grows = false;
 #pragma unroll
       for (int n = 0; n < NH; ++n) grows |= x[n][0] > m[n][0] || x[n][1] > m[n][1];

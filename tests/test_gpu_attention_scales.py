@@ -1,0 +1,32 @@
+"""The cache's scales at their ends: zeros, and blocks of very different size."""
+
+import math
+
+import pytest
+import torch
+
+import attention_reference as ref
+import test_gpu_kv_cache as kv
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("bs", [16, 32, 64, 128])
+@pytest.mark.parametrize("hq", [2, 24])
+def test_a_v_scale_of_zero_leaves_its_block_out_whatever_its_codes_are(hq, bs, d):
+    """Blocks whose V scale is 0 (or negative, or NaN) and whose codes are NaN, against a table without these blocks."""
+    from expert_major_chunked_gb300 import attention
+    lens = [9 * bs + 5, bs, 3 * bs - 1]
+    q, dev, table, kv_lens, _ = kv.decode_case(lens, hq, 2, d, bs)
+    without = table.clone()
+    out_of = [(0, 0, 0.0), (0, 4, -1.0), (0, 5, math.nan), (0, 9, 0.0), (1, 0, 0.0), (2, 1, -0.0)]
+    for b, i, scale in out_of:
+        block = int(table[b, i])
+        dev.v_scale[block] = scale
+        for codes in dev[:2]:
+            codes.view(torch.uint8)[block] = 0x7F
+        without[b, i] = -1
+    got, want = attention.decode(q, dev, table, kv_lens), attention.decode(q, dev, without, kv_lens)
+    assert torch.isfinite(want[0]).all() and not want[0][1].any() and (want[1][1] == -math.inf).all()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
