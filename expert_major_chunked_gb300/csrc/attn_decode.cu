@@ -219,7 +219,8 @@ __global__ void __launch_bounds__(kDecThreads, 2) decode_kernel(const __grid_con
       cp_async_commit();
     };
     // The queries' loads go out before the first codes are waited for. They become f16, each row scaled by a power of two
-    // to below 2 (bf16 has a wider exponent).
+    // to below 2^15: f16 is normal from 2^-14 on, so a value keeps 11 bits down to 2^-28 of the row's largest (with the
+    // largest below 2 an f16 query of 0.25 beside one of 60000 lost bits).
     constexpr int QR = 8 * NH / kDecWarps, W = D / 64;
     uint32_t qw[QR][W];
 #pragma unroll
@@ -245,8 +246,8 @@ __global__ void __launch_bounds__(kDecThreads, 2) decode_kernel(const __grid_con
 #pragma unroll
       for (int d = 16; d; d >>= 1) big = fmaxf(big, __shfl_xor_sync(~0u, big, d));
       const int e = min(max(static_cast<int>(__float_as_uint(big) >> 23), 27), 227) - 127;
-      const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-      const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+      const float down = __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);
+      const float up = __uint_as_float(static_cast<uint32_t>(127 - 14 + e) << 23);
 #pragma unroll
       for (int w = 0; w < W; ++w)
         *reinterpret_cast<uint32_t*>(q_sh + r * (D + 8) + 2 * (lane + 32 * w)) = F16::pack(x[w].x * down, x[w].y * down);

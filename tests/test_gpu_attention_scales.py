@@ -30,3 +30,22 @@ def test_a_v_scale_of_zero_leaves_its_block_out_whatever_its_codes_are(hq, bs, d
     got, want = attention.decode(q, dev, table, kv_lens), attention.decode(q, dev, without, kv_lens)
     assert torch.isfinite(want[0]).all() and not want[0][1].any() and (want[1][1] == -math.inf).all()
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("dtype,large", [(torch.float16, 60000.0), (torch.bfloat16, 2.0 ** 20)])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_decode_queries_with_one_large_channel(d, dtype, large):
+    """One channel of the query is large where the keys have zeros, so that the scores come from the others: these keep
+    their bits (the bound has no term for the conversion to f16: it is exact down to 2^-28 of the row's largest)."""
+    from expert_major_chunked_gb300 import attention
+    lens, hq, hk, bs = [150, 40], 4, 2, 16
+    q, dev, table, kv_lens, (kc, vc, ks, vs, tt) = kv.decode_case(lens, hq, hk, d, bs, dtype, stale=False)
+    g = torch.Generator().manual_seed(d)
+    q = (0.25 * torch.randn(q.shape, generator=g)).to(dtype).cuda()
+    q[..., 5] = large
+    kc[..., 5] = 0.0
+    dev.k.view(torch.uint8)[..., 5] = 0
+    ks = torch.exp2(torch.randint(-2, 2, ks.shape, generator=g).double())
+    dev = dev._replace(k_scale=ks.float().cuda())
+    out, lse = attention.decode(q, dev, table, kv_lens)
+    ref.check(out, lse.T, ref.decode(q, kc, vc, ks, vs, tt, lens, 1 / math.sqrt(d)), ref.U[torch.float16])
