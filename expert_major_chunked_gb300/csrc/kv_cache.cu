@@ -266,7 +266,7 @@ __device__ __forceinline__ void store_codes(uint8_t* dst, const Words<V>& x, flo
   if constexpr (V == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
 }
 
-// codes of one row times ratio (a power of two below 1)
+// codes of one row times ratio (below 1: a power of two, or 0 where the old scale was 0 and so were the values)
 template <int V>
 __device__ __forceinline__ void rescale_row(uint8_t* row, float ratio) {
 #pragma unroll
@@ -408,7 +408,7 @@ __global__ void __launch_bounds__(kAppendThreads, HOLD * D <= 1024 ? kAppendCtas
     const float want = pow2i(scale_log2(run_amax(len)));  // (its barrier: the old scale is read before it is written)
     const float scale = off > 0 && old >= want ? old : want, inv = 1.0f / scale;
     uint8_t* base = codes + (at << BLOCK_LOG2) * D;
-    if (off > 0 && scale > old && old > 0.0f)
+    if (off > 0 && scale > old && old >= 0.0f)
       for (int r = warp; r < off; r += kAppendWarps) rescale_row<V>(base + r * D, old / scale);
     if (threadIdx.x == 0) scales[at] = scale;
 #pragma unroll
@@ -459,7 +459,7 @@ __global__ void __launch_bounds__(kAppendThreads, HOLD * D <= 1024 ? kAppendCtas
     const float scale = off > 0 && old >= want ? old : want;
     uint8_t* base = codes + (at << BLOCK_LOG2) * D;
     if (i == s) {
-      if (off > 0 && scale > old && old > 0.0f)  // the codes that are there, for the larger scale
+      if (off > 0 && scale > old && old >= 0.0f)  // the codes that are there, for the larger scale
         for (int r = 0; r < off; ++r) rescale_row<V>(base + r * D, old / scale);
       if (lane == 0) scales[at] = scale;
     }

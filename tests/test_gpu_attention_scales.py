@@ -49,3 +49,22 @@ def test_decode_queries_with_one_large_channel(d, dtype, large):
     dev = dev._replace(k_scale=ks.float().cuda())
     out, lse = attention.decode(q, dev, table, kv_lens)
     ref.check(out, lse.T, ref.decode(q, kc, vc, ks, vs, tt, lens, 1 / math.sqrt(d)), ref.U[torch.float16])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("bs,d", [(16, 64), (32, 128), (64, 256), (128, 128)])
+@pytest.mark.parametrize("tokens", [1, 9, 300])
+def test_append_behind_tokens_of_scale_zero(tokens, bs, d, dtype):
+    """Blocks whose tokens have a scale of 0: their values are 0 whatever the codes, and stay 0 under the new scale."""
+    from expert_major_chunked_gb300 import attention
+    blocks = tokens + 3
+    dev, *host = kv.cache(blocks, 2, bs, d)
+    slots = ([b * bs + 7 for b in range(tokens)] if tokens < 10 else  # single tokens, or runs over blocks' borders
+             [b * bs + 5 + i for b in range(0, 60) for i in range(5)])
+    for scale, h in ((dev.k_scale, host[2]), (dev.v_scale, host[3])):
+        scale[::2], h[::2] = 0.0, 0.0
+    k, v = kv.rows(len(slots), 2, d, dtype, bs)
+    attention.append(k, v, kv.ints(slots, torch.int64), dev)
+    ref.append(k.cpu(), slots, host[0], host[2])
+    ref.append(v.cpu(), slots, host[1], host[3])
+    kv.same_cache(dev, *host)
