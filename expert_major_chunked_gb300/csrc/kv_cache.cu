@@ -18,8 +18,6 @@ namespace {
 constexpr int kAssignThreads = 512, kAssignWarps = kAssignThreads / 32;
 constexpr int kAssignPiece = 128;  // table entries that a warp writes at a time: 16 bytes a lane
 
-__device__ __forceinline__ int32_t sat32(long long v) { return v > 0x7FFFFFFFll ? 0x7FFFFFFF : static_cast<int32_t>(v); }
-
 // Sums stop at 2^31 - 1 (so added, values from 0 to there may be added in any order).
 __device__ __forceinline__ uint32_t sat_add(uint32_t x, uint32_t y) { return min(x + y, 0x7FFFFFFFu); }
 // the lanes' sum
@@ -130,8 +128,9 @@ __global__ void __launch_bounds__(kAssignThreads) kv_assign_kernel(const __grid_
         const int mid = (lo + hi + 1) >> 1;
         if (tok0[mid] <= t) lo = mid; else hi = mid - 1;
       }
-      pos = sat32(ctx[lo] + (t - tok0[lo]));
-      const uint32_t c = static_cast<uint32_t>(pos) / bs, n0 = blocks_held(lo);
+      const uint32_t at = ctx[lo] + static_cast<uint32_t>(t - tok0[lo]);  // below 2^32: its slot is right past 2^31 too
+      pos = static_cast<int>(min(at, 0x7FFFFFFFu));
+      const uint32_t c = at / bs, n0 = blocks_held(lo);
       int id = -1;
       if (c < static_cast<uint32_t>(a.max_blocks)) {
         if (c < n0) {
@@ -141,7 +140,7 @@ __global__ void __launch_bounds__(kAssignThreads) kv_assign_kernel(const __grid_
           if (f < a.n_free) id = a.free_blocks[f];
         }
       }
-      if (id >= 0) slot = static_cast<long long>(id) * bs + static_cast<uint32_t>(pos) % bs;
+      if (id >= 0) slot = static_cast<long long>(id) * bs + at % bs;
     }
     a.slot_map[t] = slot;
     a.positions[t] = pos;

@@ -82,7 +82,8 @@ moe_status moe_attn_check(void* stream);
  *                       block does not exist (free_blocks exhausted, or past max_blocks)
  *   positions[max_tokens]  token -> its position in the request; -1 past the last token
  *   used[1]             blocks needed beyond those held (more than n_free: the pool was too small)
- * Calling it again with the same arguments gives the same outputs. n_requests <= 16384.
+ * Lengths, sums and positions stop at 2^31 - 1; slots do not. Calling it again with the same arguments gives the same
+ * outputs. n_requests <= 16384.
  */
 typedef struct {
   const int32_t* ctx_lens;     /* [n_requests] */

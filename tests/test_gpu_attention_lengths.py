@@ -53,3 +53,20 @@ def test_prefill_tiles_that_take_seconds():
     out, lse = attention.prefill(q, k, v, kv.ints([0, 1]), kv.ints([0, n]), scale=1.0)
     attention.raise_on_device_error()
     assert torch.equal(out[0, 0], v[key, 0]) and abs(lse.item() - 200.0) < 1e-3
+
+
+@pytest.mark.parametrize("bs", [1 << 30, (1 << 29) + 5])
+def test_assign_slots_of_positions_past_int32(bs):
+    """A request that passes 2^31 tokens: positions stop at 2^31 - 1, slots go on in the next block."""
+    from expert_major_chunked_gb300 import attention
+    top = (1 << 31) - 1
+    ctx, new, mb = top - 4, 10, 6
+    held = -(-ctx // bs)
+    table = kv.ints([[3 + i if i < held else -1 for i in range(mb)]])
+    s = attention.assign_slots(kv.ints([ctx]), kv.ints([new]), kv.ints([20, 21, 22]), table, bs, 12)
+    row = [3 + i for i in range(held)] + [20] * (-(-(ctx + new) // bs) - held)
+    at = range(ctx, ctx + new)
+    assert table[0].tolist() == row + [-1] * (mb - len(row))
+    assert s.positions.tolist() == [min(p, top) for p in at] + [-1, -1]
+    assert s.slot_map.tolist() == [row[p // bs] * bs + p % bs for p in at] + [-1, -1]
+    assert s.kv_lens.tolist() == [top] and s.cu_new.tolist() == [0, new]
