@@ -62,7 +62,7 @@ def _load():
     with _lock:
         if _native is None:
             _b.lib()  # builds and loads libmoe_prefill.so
-            spec = importlib.util.spec_from_file_location("attention_py", _build.EXT_PATH)
+            spec = importlib.util.spec_from_file_location("attention_py", _build.build_extension())
             module = importlib.util.module_from_spec(spec)
             spec.loader.exec_module(module)
             _native = module

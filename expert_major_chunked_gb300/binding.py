@@ -125,7 +125,7 @@ def lib(build_if_needed: bool = True):
     global _lib
     with _lock:
         if _lib is None:
-            path = _build.build() if build_if_needed else _build.LIB_PATH
+            path = _build.build(extension=False) if build_if_needed else _build.LIB_PATH
             L = ctypes.CDLL(path)
             for name, (args, res) in _SIGS.items():
                 fn = getattr(L, name)
