@@ -14,6 +14,7 @@ The operators are for serving: no gradients are recorded, whatever the inputs as
 from __future__ import annotations
 
 import importlib.util
+import operator
 import threading
 from typing import NamedTuple, Optional
 
@@ -50,6 +51,7 @@ class Slots(NamedTuple):
 _DTYPES = (torch.bfloat16, torch.float16)
 _CODES = (torch.float8_e4m3fn, torch.uint8)
 _I32, _I64, _F32 = torch.int32, torch.int64, torch.float32
+_MAX = (1 << 31) - 1
 _lock = threading.Lock()
 _native = None
 
@@ -69,7 +71,15 @@ def _load():
     return _native
 
 
+def _tensor(name, t):
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name} must be a tensor, not {type(t).__name__}")
+    if max(t.shape, default=0) > _MAX:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}: sizes must be below 2^31")
+
+
 def _rows(name, t, dtype=None, shape=None):
+    _tensor(name, t)
     if t.dim() != 3 or not t.is_cuda or t.dtype not in _DTYPES or t.stride(2) != 1:
         raise ValueError(f"{name} must be a [tokens][heads][head_dim] CUDA tensor, bf16 or f16, head_dim dense")
     if dtype is not None and t.dtype != dtype:
@@ -79,6 +89,7 @@ def _rows(name, t, dtype=None, shape=None):
 
 
 def _ints(name, t, dtype=_I32, dim=1):
+    _tensor(name, t)
     if t.dtype != dtype or t.dim() != dim or not t.is_cuda or (t.stride(-1) != 1 and t.shape[-1] > 1):
         raise ValueError(f"{name} must be a {dim}-D {dtype} CUDA tensor with dense rows")
 
@@ -86,12 +97,34 @@ def _ints(name, t, dtype=_I32, dim=1):
 def _results(q, out, lse, lse_shape):
     if out is not None:
         _rows("out", out, q.dtype, q.shape)
+    if lse is not None:
+        _tensor("lse", lse)
     if lse is not None and (lse.dtype != _F32 or tuple(lse.shape) != lse_shape or not lse.is_contiguous()):
         raise ValueError(f"lse must be a contiguous float32 tensor of shape {lse_shape}")
 
 
+def _scale(scale):
+    try:
+        float(1.0 if scale is None else scale)
+    except (TypeError, ValueError, OverflowError, RuntimeError):
+        raise ValueError(f"scale must be a number, not {scale!r}") from None
+
+
+def _size(name, v):
+    try:
+        v = operator.index(v)
+    except TypeError:
+        raise ValueError(f"{name} must be a whole number, not {v!r}") from None
+    if not 0 <= v <= _MAX:
+        raise ValueError(f"{name} is {v}: it must be from 0 to 2^31 - 1")
+
+
 def _cache(cache):
+    if not isinstance(cache, tuple) or len(cache) != 4:
+        raise ValueError("cache must be a KvCache, or a tuple of its four tensors")
     k, v, ks, vs = cache
+    for name, t in zip(KvCache._fields, cache):
+        _tensor(f"the cache's {name}", t)
     if k.dim() != 4 or k.dtype not in _CODES or v.shape != k.shape or v.dtype != k.dtype:
         raise ValueError("the cache's codes must be two [blocks][kv heads][block size][head dim] tensors, "
                          "float8_e4m3fn or uint8")
@@ -123,7 +156,7 @@ def _elsewhere(call, device, stream, tensors, *args):
     """call(*args) with `device`, or `stream` where there is one, current; the tensors are marked as used there."""
     if stream is None:
         if torch.cuda.current_device() == device.index:
-            raise ValueError("scale, block_size and max_tokens must be numbers (max_tokens from 0), sizes below 2^31")
+            raise ValueError("an argument is not of the kind that the call takes")
         with torch.cuda.device(device):
             return call(*args)
     if stream.device != device:
@@ -159,6 +192,7 @@ def prefill(q, k, v, cu_q, cu_k=None, scale: Optional[float] = None, out=None, l
     _ints("cu_k", cu_k)
     if cu_q.shape[0] < 1 or cu_q.shape != cu_k.shape:
         raise ValueError("cu_q and cu_k must both have one entry more than there are sequences")
+    _scale(scale)
     _results(q, out, lse, (q.shape[1], q.shape[0]))
     _same_device(q=q, k=k, v=v, cu_q=cu_q, cu_k=cu_k, out=out, lse=lse)
     return _elsewhere(prefill, q.device, stream, (q, k, v, cu_q, cu_k, out, lse), q, k, v, cu_q, cu_k, scale, out, lse)
@@ -185,6 +219,8 @@ def assign_slots(ctx_lens, new_lens, free_blocks, block_table, block_size: int, 
     _ints("block_table", block_table, dim=2)
     if not ctx_lens.shape[0] == new_lens.shape[0] == block_table.shape[0]:
         raise ValueError("ctx_lens, new_lens and block_table must have one row a request")
+    _size("block_size", block_size)
+    _size("max_tokens", max_tokens)
     _same_device(ctx_lens=ctx_lens, new_lens=new_lens, free_blocks=free_blocks, block_table=block_table)
     return _elsewhere(assign_slots, ctx_lens.device, stream, (ctx_lens, new_lens, free_blocks, block_table), ctx_lens,
                       new_lens, free_blocks, block_table, block_size, max_tokens)
@@ -232,7 +268,10 @@ def decode(q, cache: KvCache, block_table, kv_lens, scale: Optional[float] = Non
         raise ValueError(f"the cache has head_dim {kc.shape[3]}, q has {q.shape[2]}")
     if not block_table.shape[0] == kv_lens.shape[0] == q.shape[0]:
         raise ValueError("block_table and kv_lens must have one row a request")
+    _scale(scale)
     _results(q, out, lse, tuple(q.shape[:2]))
+    if workspace is not None:
+        _tensor("workspace", workspace)
     if workspace is not None and (workspace.dtype != torch.uint8 or not workspace.is_contiguous()):
         raise ValueError("workspace must be a contiguous uint8 tensor")
     _same_device(q=q, block_table=block_table, kv_lens=kv_lens, cache_k=kc, cache_v=vc, k_scale=ks, v_scale=vs, out=out,

@@ -73,3 +73,33 @@ def test_an_error_that_is_there_is_not_the_calls_own():
 
 def test_a_call_that_fails_leaves_no_error():
     run("attention.raise_on_device_error,", "assert torch.equal(layer.run(inp['x'], 16), want_y)")
+
+
+def test_refusals_name_the_argument():
+    """What the calls on tensors do not take, with the argument that is to blame in the message."""
+    import torch
+
+    import test_gpu_kv_cache as kv
+    from expert_major_chunked_gb300 import attention
+    q, dev, table, lens, _ = kv.decode_case([5, 7], 4, 2, 64, 16)
+    x, cu, slots = q[:, :2].contiguous(), kv.ints([0, 2]), kv.ints([0, 1], torch.int64)
+    for name, call in (
+            ("cache", lambda: attention.decode(q, list(dev), table, lens)),
+            ("cache", lambda: attention.append(x, x, slots, list(dev))),
+            ("cache", lambda: attention.append(x, x, slots, dev[:3])),
+            ("v_scale", lambda: attention.append(x, x, slots, dev._replace(v_scale=1.0))),
+            ("scale", lambda: attention.prefill(q, x, x, cu, scale="x")),
+            ("scale", lambda: attention.decode(q, dev, table, lens, scale=[1.0])),
+            ("block_size", lambda: attention.assign_slots(lens, lens, lens, table, 16.0, 4)),
+            ("block_size", lambda: attention.assign_slots(lens, lens, lens, table, -16, 4)),
+            ("max_tokens", lambda: attention.assign_slots(lens, lens, lens, table, 16, 1 << 31)),
+            ("max_tokens", lambda: attention.assign_slots(lens, lens, lens, table, 16, None)),
+            ("k", lambda: attention.prefill(q, None, x, cu)), ("out", lambda: attention.prefill(q, x, x, cu, out=3)),
+            ("lse", lambda: attention.decode(q, dev, table, lens, lse=3)),
+            ("workspace", lambda: attention.decode(q, dev, table, lens, workspace=3)),
+            ("slot_map", lambda: attention.append(x, x, [0, 1], dev)),
+            ("kv_lens", lambda: attention.decode(q, dev, table, [5, 7]))):
+        with pytest.raises(ValueError, match=rf"\b{name}\b"):
+            call()
+    with pytest.raises(ValueError, match="below 2"):
+        attention.assign_slots(lens[:1].expand(1 << 31), lens, lens, table, 16, 4)
