@@ -8,7 +8,8 @@
 Every call enqueues kernels of libmoe_prefill.so on `stream` (default: the current stream) and returns at once. Results
 and scratch are allocated for that stream; where it is not the current stream, the caller orders its inputs before it
 (a wait on an event) and the results after it, and the tensors given are marked as used there.
-The operators are for serving: no gradients are recorded, whatever the inputs ask for.
+The operators are for serving and have no backward pass. Where an input asks for gradients, results that the call allocates
+raise an error when gradients are taken through them; buffers that are given for results, and the cache, have none.
 """
 
 from __future__ import annotations
@@ -168,6 +169,29 @@ def _elsewhere(call, device, stream, tensors, *args):
         return call(*args)
 
 
+class _NoBackward(torch.autograd.Function):
+    """A result as it is, with the inputs behind it."""
+
+    @staticmethod
+    def forward(ctx, result, *inputs):
+        return result.detach()
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise RuntimeError("the attention operators have no backward pass: they are for serving")
+
+
+def _wants_grad(*inputs):
+    return torch.is_grad_enabled() and any(t.requires_grad for t in inputs)
+
+
+def _without_backward(call, inputs, out, lse, *args):
+    """call(*args)'s (out, lse); those that were not given raise where gradients are taken through them."""
+    with torch.no_grad():
+        results = call(*args)
+    return tuple(r if given is not None else _NoBackward.apply(r, *inputs) for r, given in zip(results, (out, lse)))
+
+
 def prefill(q, k, v, cu_q, cu_k=None, scale: Optional[float] = None, out=None, lse=None, stream=None):
     """Causal attention over packed sequences; returns (out [tokens][heads][dim], lse float32 [heads][tokens]).
 
@@ -195,6 +219,8 @@ def prefill(q, k, v, cu_q, cu_k=None, scale: Optional[float] = None, out=None, l
     _scale(scale)
     _results(q, out, lse, (q.shape[1], q.shape[0]))
     _same_device(q=q, k=k, v=v, cu_q=cu_q, cu_k=cu_k, out=out, lse=lse)
+    if _wants_grad(q, k, v):
+        return _without_backward(prefill, (q, k, v), out, lse, q, k, v, cu_q, cu_k, scale, out, lse, stream)
     return _elsewhere(prefill, q.device, stream, (q, k, v, cu_q, cu_k, out, lse), q, k, v, cu_q, cu_k, scale, out, lse)
 
 
@@ -276,6 +302,8 @@ def decode(q, cache: KvCache, block_table, kv_lens, scale: Optional[float] = Non
         raise ValueError("workspace must be a contiguous uint8 tensor")
     _same_device(q=q, block_table=block_table, kv_lens=kv_lens, cache_k=kc, cache_v=vc, k_scale=ks, v_scale=vs, out=out,
                  lse=lse, workspace=workspace)
+    if _wants_grad(q):
+        return _without_backward(decode, (q,), out, lse, q, cache, block_table, kv_lens, scale, out, lse, workspace, stream)
     return _elsewhere(decode, q.device, stream, (q, block_table, kv_lens, out, lse, workspace, *cache), q, cache,
                       block_table, kv_lens, scale, out, lse, workspace)
 

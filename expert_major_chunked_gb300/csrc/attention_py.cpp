@@ -1,13 +1,15 @@
 // The attention operators' calls on torch tensors (a Python extension module): argument tests, results and scratch, and
 // the C entries of include/moe_attention.h. attention.py documents the operators and says what is wrong with arguments
-// that are not taken here: a function returns None for those (also when the tensors' device is not the current one), the
-// status for a call that the library refuses, and the results otherwise.
+// that are not taken here: a function returns None for those (also when the tensors' device is not the current one, or
+// where gradients are asked for), the status for a call that the library refuses, and the results otherwise. Tensors that
+// a call changes have their version counted up, as autograd expects of changes in place.
 //
 // A decode step is a few kernels of a few microseconds each, so what a call costs on the host counts: the same tests,
 // allocations and marshalling written in Python took 9 us of a prefill call and 11 us of a decode call.
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
+#include <ATen/core/grad_mode.h>
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGraphsC10Utils.h>
@@ -86,6 +88,11 @@ Tensor empty(at::IntArrayRef sizes, at::ScalarType type, const Tensor& like) {
   return at::detail::empty_cuda(sizes, type, like.device(), std::nullopt);
 }
 
+bool wants_grad(const Tensor& t) { return t.requires_grad() && at::GradMode::is_enabled(); }
+void changed(const Tensor& t) {
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 struct Cache {
   const Tensor *k, *v, *ks, *vs;
 };
@@ -117,7 +124,8 @@ PyObject* prefill(PyObject*, PyObject* const* arg, Py_ssize_t n) {
       v->sizes() != k->sizes() || k->size(2) != q->size(2) || !is_ints(cq, 1, at::kInt, q->get_device()) ||
       !is_ints(ck, 1, at::kInt, q->get_device()) || cq->size(0) < 1 || ck->size(0) != cq->size(0) ||
       !scale_of(arg[5], q->size(2), a.scale) || !optional(arg[6], out_given) || !optional(arg[7], lse_given) ||
-      !fits(q->size(0)) || !fits(k->size(0)) || !fits(cq->size(0)) || !fits(q->size(1)) || !fits(k->size(1)))
+      !fits(q->size(0)) || !fits(k->size(0)) || !fits(cq->size(0)) || !fits(q->size(1)) || !fits(k->size(1)) ||
+      wants_grad(*q) || wants_grad(*k) || wants_grad(*v))
     return none();
   if (out_given && (!is_rows(out_given, *q) || out_given->sizes() != q->sizes())) return none();
   if (lse_given && (lse_given->scalar_type() != at::kFloat || lse_given->dim() != 2 ||
@@ -138,6 +146,8 @@ PyObject* prefill(PyObject*, PyObject* const* arg, Py_ssize_t n) {
   a.head_dim = static_cast<int32_t>(q->size(2));
   const moe_status st = moe_attn_prefill(&a, stream_of(*q));
   if (st != MOE_OK) return PyLong_FromLong(st);
+  if (out_given) changed(out);
+  if (lse_given) changed(lse);
   return Py_BuildValue("(NN)", THPVariable_Wrap(out), THPVariable_Wrap(lse));
   END_HANDLE_TH_ERRORS
 }
@@ -170,6 +180,7 @@ PyObject* assign(PyObject*, PyObject* const* arg, Py_ssize_t n) {
   a.max_blocks = static_cast<int32_t>(table->size(1));
   const moe_status st = moe_kv_assign(&a, stream_of(*ctx));
   if (st != MOE_OK) return PyLong_FromLong(st);
+  changed(*table);
   return Py_BuildValue("(NNNNN)", THPVariable_Wrap(cu_new), THPVariable_Wrap(kv_lens), THPVariable_Wrap(slots),
                        THPVariable_Wrap(positions), THPVariable_Wrap(used));
   END_HANDLE_TH_ERRORS
@@ -195,6 +206,7 @@ PyObject* append(PyObject*, PyObject* const* arg, Py_ssize_t n) {
   a.block_size = static_cast<int32_t>(c.k->size(2)), a.num_blocks = static_cast<int32_t>(c.k->size(0));
   const moe_status st = moe_kv_append(&a, stream_of(*k));
   if (st != MOE_OK) return PyLong_FromLong(st);
+  for (const Tensor* t : {c.k, c.v, c.ks, c.vs}) changed(*t);
   Py_RETURN_TRUE;
   END_HANDLE_TH_ERRORS
 }
@@ -222,7 +234,8 @@ PyObject* decode(PyObject*, PyObject* const* arg, Py_ssize_t n) {
       c.k->size(3) != q->size(2) || !is_ints(table, 2, at::kInt, q->get_device()) ||
       !is_ints(lens, 1, at::kInt, q->get_device()) || table->size(0) != q->size(0) || lens->size(0) != q->size(0) ||
       !scale_of(arg[4], q->size(2), a.scale) || !optional(arg[5], out_given) || !optional(arg[6], lse_given) ||
-      !optional(arg[7], ws_given) || !fits(q->size(0)) || !fits(q->size(1)) || !fits(table->size(1)))
+      !optional(arg[7], ws_given) || !fits(q->size(0)) || !fits(q->size(1)) || !fits(table->size(1)) ||
+      wants_grad(*q))
     return none();
   if (out_given && (!is_rows(out_given, *q) || out_given->sizes() != q->sizes())) return none();
   if (lse_given && (lse_given->scalar_type() != at::kFloat || lse_given->sizes() != q->sizes().slice(0, 2) ||
@@ -251,6 +264,8 @@ PyObject* decode(PyObject*, PyObject* const* arg, Py_ssize_t n) {
   a.max_blocks = static_cast<int32_t>(table->size(1));
   const moe_status st = moe_attn_decode(&a, stream);
   if (st != MOE_OK) return PyLong_FromLong(st);
+  if (out_given) changed(out);
+  if (lse_given) changed(lse);
   return Py_BuildValue("(NN)", THPVariable_Wrap(out), THPVariable_Wrap(lse));
   END_HANDLE_TH_ERRORS
 }
