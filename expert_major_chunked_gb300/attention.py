@@ -225,9 +225,11 @@ def prefill(q, k, v, cu_q, cu_k=None, scale: Optional[float] = None, out=None, l
 
 
 def raise_on_device_error(stream=None) -> None:
-    """Waits for the stream and raises MoeError when a wait inside a prefill kernel has given up since the last check."""
+    """Waits for the stream and raises MoeError when a wait inside a prefill kernel on its device has given up since the
+    last check."""
     s = stream if stream is not None else torch.cuda.current_stream()
-    _b._check(_b.lib().moe_attn_check(s.cuda_stream))
+    with torch.cuda.device(s.device):
+        _b._check(_b.lib().moe_attn_check(s.cuda_stream))
 
 
 def assign_slots(ctx_lens, new_lens, free_blocks, block_table, block_size: int, max_tokens: int, stream=None) -> Slots:

@@ -70,3 +70,30 @@ def test_calls_on_a_second_device():
                                           *attention.decode(q[-1:], cache, table, cu[1:]))])
     for a, b in zip(*results):
         assert torch.equal(a, b)
+
+
+def test_the_error_check_runs_on_the_streams_device(monkeypatch):
+    """Its word is the current device's, which need not be the stream's. (Stand-ins for torch's device switch, the
+    stream and the library.)"""
+    from types import SimpleNamespace
+
+    from expert_major_chunked_gb300 import attention
+    current, asked = ["cuda:0"], []
+
+    class Device:
+        def __init__(self, device):
+            self.device = device
+
+        def __enter__(self):
+            self.before, current[0] = current[0], self.device
+
+        def __exit__(self, *exc):
+            current[0] = self.before
+
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(attention._b, "lib", lambda: SimpleNamespace(
+        moe_attn_check=lambda stream: asked.append((current[0], stream)) or 0))
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: SimpleNamespace(device="cuda:0", cuda_stream=7))
+    attention.raise_on_device_error(SimpleNamespace(device="cuda:1", cuda_stream=5))
+    attention.raise_on_device_error()
+    assert asked == [("cuda:1", 5), ("cuda:0", 7)] and current == ["cuda:0"]
