@@ -68,3 +68,31 @@ def test_append_behind_tokens_of_scale_zero(tokens, bs, d, dtype):
     ref.append(k.cpu(), slots, host[0], host[2])
     ref.append(v.cpu(), slots, host[1], host[3])
     kv.same_cache(dev, *host)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("bs", [16, 64])
+@pytest.mark.parametrize("hq,hk", [(4, 2), (24, 2)])
+def test_scales_apart(hq, hk, bs, d):
+    """Blocks of a large V scale and small codes beside ones of a small scale and large codes, to the reference's own bound
+    (test_attention_scales_plain.py shows that weights of up to 1 would not meet it)."""
+    from expert_major_chunked_gb300 import attention
+    from test_attention_scales_plain import scales_apart
+    q, kc, vc, ks, vs, table, lens = scales_apart(hq, hk, d, bs, 900, d)
+    dev = attention.KvCache(*(x.float().to(torch.float8_e4m3fn).cuda() for x in (kc, vc)),
+                            *(x.float().cuda() for x in (ks, vs)))
+    out, lse = attention.decode(q.cuda(), dev, table.int().cuda(), kv.ints(lens))
+    ref.check(out, lse.T, ref.decode(q, kc, vc, ks, vs, table, lens, 1 / math.sqrt(d)), ref.U[torch.float16])
+
+
+def test_scales_of_all_sizes_to_the_references_bound():
+    """V scales from 2^-30 to 2^30, K scales that are no powers of two."""
+    from expert_major_chunked_gb300 import attention
+    for d, lens in ((64, [300, 77]), (128, [300, 77]), (256, [500])):
+        q, dev, table, kv_lens, (kc, vc, ks, vs, tt) = kv.decode_case(lens, 4, 2, d, 16)
+        g = torch.Generator().manual_seed(5)
+        vs = torch.exp2(torch.randint(-30, 31, vs.shape, generator=g).double())
+        ks = (ks * (1 + torch.rand(ks.shape, generator=g).double())).float().double()
+        dev = dev._replace(v_scale=vs.float().cuda(), k_scale=ks.float().cuda())
+        out, lse = attention.decode(q, dev, table, kv_lens)
+        ref.check(out, lse.T, ref.decode(q, kc, vc, ks, vs, tt, lens, 1 / math.sqrt(d)), ref.U[torch.float16])
