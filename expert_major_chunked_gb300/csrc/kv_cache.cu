@@ -469,7 +469,7 @@ __global__ void __launch_bounds__(kAppendThreads, HOLD * D <= 1024 ? kAppendCtas
 template <class T, int D>
 cudaError_t append_dim(const moe_kv_append_args& a, cudaStream_t stream) {
   const int window = a.n_tokens <= kAppendShort ? kAppendWarps : a.block_size;
-  const dim3 grid((a.n_tokens + window - 1) / window, a.n_kv_heads, 2);
+  const dim3 grid((static_cast<uint32_t>(a.n_tokens) + window - 1) / window, a.n_kv_heads, 2);
   switch (a.block_size) {
     case 16: return launch_early(kv_append_kernel<T, D, 2>, grid, dim3(kAppendThreads), 0, stream, a, window);
     case 32: return launch_early(kv_append_kernel<T, D, 4>, grid, dim3(kAppendThreads), 0, stream, a, window);

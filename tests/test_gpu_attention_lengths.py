@@ -70,3 +70,20 @@ def test_assign_slots_of_positions_past_int32(bs):
     assert s.positions.tolist() == [min(p, top) for p in at] + [-1, -1]
     assert s.slot_map.tolist() == [row[p // bs] * bs + p % bs for p in at] + [-1, -1]
     assert s.kv_lens.tolist() == [top] and s.cu_new.tolist() == [0, new]
+
+
+@pytest.mark.parametrize("bs", [16, 128])
+def test_append_up_to_the_last_int32(bs):
+    """2^31 - 1 tokens (one row, expanded), all without a slot but the first and the last ones."""
+    from expert_major_chunked_gb300 import attention
+    n, d = (1 << 31) - 1, 64
+    dev, small = (attention.KvCache.empty(4, 1, bs, d) for _ in range(2))
+    row = torch.randn(1, 1, d, generator=torch.Generator().manual_seed(bs)).to(torch.bfloat16).cuda()
+    slots = torch.full((n,), -1, dtype=torch.int64, device="cuda")
+    ends = [bs + 1, bs + 2, 2 * bs, 2 * bs + 1, 2 * bs + 2]
+    slots[:2], slots[-3:] = kv.ints(ends[:2], torch.int64), kv.ints(ends[2:], torch.int64)
+    attention.append(row.expand(n, 1, d), row.expand(n, 1, d), slots, dev)
+    attention.append(row.expand(5, 1, d), row.expand(5, 1, d), kv.ints(ends, torch.int64), small)
+    for a, b in zip(dev, small):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    assert dev.k.float()[1, 0, 1:3].abs().sum() > 0 and dev.k.float()[2, 0, :3].abs().sum() > 0
