@@ -1016,6 +1016,13 @@ __global__ void __launch_bounds__(kTThreads, 1) prefill_kernel(const __grid_cons
           l += t2.x + t2.y;
         }
         steps += nt;
+        // With one sub-tile the last scores were asked for before the last but one product with V, so that product may not be
+        // done here. A barrier tells apart two phases only, so both have to be waited for, one after the other. (With two
+        // sub-tiles each one's scores come after its product before.)
+        if (NQ == 1 && ok && nt > 1) {
+          ok = wait_working(pv_done, steps & 1u, flags);
+          ok = __all_sync(~0u, ok);
+        }
         if (ok && nt > 0) {
           ok = wait_working(pv_done + 8u * sub, (steps - 1u) & 1u, flags);
           ok = __all_sync(~0u, ok);
