@@ -15,10 +15,10 @@
 // order, always the same, so that the same call gives the same bytes.
 //
 // What bounds it: the bytes of the cache, 2 head_dim a token and kv head, each read once. 64 requests of up to 16384
-// tokens, 32 query heads on 8 kv heads of 128: 1.1 GB in 172 us, 6.4 TB/s, 94% of a plain copy's rate. One request of
-// 131072 tokens, 16 heads on 2 of 256 (134 MB): 30.6 us, of which about 8 us are the two launches, the first loads'
+// tokens, 32 query heads on 8 kv heads of 128: 1.1 GB in 174 us, 6.3 TB/s, 93% of a plain copy's rate. One request of
+// 131072 tokens, 16 heads on 2 of 256 (134 MB): 30.4 us, of which about 8 us are the two launches, the first loads'
 // latency and the join (20 us would be the bytes alone; two stages a warp and two CTAs an SM measured best, against 3 x 2,
-// 2 x 3 and 2 x 4 and against CTAs of 8 warps). One request of 1500 tokens: 6.7 us on the GPU, two launches' latency; the
+// 2 x 3 and 2 x 4 and against CTAs of 8 warps). One request of 1500 tokens: 6.6 us on the GPU, two launches' latency; the
 // host needs about 8 us to issue it. Both kernels are launched early (attn.h; 33.0 us without at 131072 tokens).
 #include "attn.h"
 #include "attn.cuh"

@@ -7,12 +7,12 @@
 // tokens (row = token * heads + head), so a tile reads its keys and values once for the whole group.
 //
 // What bounds it, head_dim 128 in bf16, one call after another:
-//   - long sequences, the two products: 16022 tokens, 16 heads on 2: 610 us, 1.72 PFLOP/s, 89% of a library product's
+//   - long sequences, the two products: 16022 tokens, 16 heads on 2: 607 us, 1.73 PFLOP/s, 90% of a library product's
 //     burst rate (the power limit holds the clock in a run of such calls). The last 2048 of as many tokens, 16 heads on
-//     4: 166 us; 128 tiles on 152 SMs, and a step of 128 keys takes 2325 cycles of which 2048 are the products.
+//     4: 168 us; 128 tiles on 152 SMs, and a step of 128 keys takes 2325 cycles of which 2048 are the products.
 //   - short sequences, the ends of tiles: 13 of them with 4099 tokens, 32 heads on 8, f16: 35 us, 2.4 TB/s; about 5 us until
 //     the first scores are there, and 2500 cycles a tile (5200 with head_dim 256) to divide and write the outputs.
-//   - a few tokens, the launch: 40 tokens 6.3 us. The launch is an early one (attn.h): it was 8.2 us without, 35 was 37.
+//   - a few tokens, the launch: 40 tokens 6.5 us. The launch is an early one (attn.h): it was 8.2 us without, 35 was 37.
 #include "attn.h"
 #include "attn.cuh"
 

@@ -14,7 +14,7 @@ namespace {
 // 7.7. (CTAs of 1024 threads, one an SM: 6.5 us against 7.0 for 1024 requests, 4.0 against 3.5 for 64.)
 // What bounds a call is the latency of that chain (lengths, sums, then table or ids) and, before it, the host, which takes
 // 8 us to issue a call (five results to allocate). On the GPU 1024 requests with tables of 2048 entries and 131072 new
-// tokens take 7.0 us, 6.8 MB; 64 requests 3.5 us.
+// tokens take 7.0 us, 6.8 MB; 64 requests 3.6 us.
 constexpr int kAssignThreads = 512, kAssignWarps = kAssignThreads / 32;
 constexpr int kAssignPiece = 128;  // table entries that a warp writes at a time: 16 bytes a lane
 
@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(kAssignThreads) kv_assign_kernel(const __grid_
 // takes the runs that begin in its window of block_size tokens; they end at most a block further on. Its warps take the
 // window's tokens in turn whatever runs they belong to, so that their rows are on their way at once: what bounds a call
 // is the latency of one chain (slots, rows and scales, barriers, codes), not the bytes. One call after another, 16022
-// tokens of 8 heads of 128 take 18.75 us, 98.6 MB, 5.3 TB/s, and 64 single tokens 3.1 us.
+// tokens of 8 heads of 128 take 18.7 us, 98.6 MB, 5.3 TB/s, and 64 single tokens 3.1 us.
 constexpr int kAppendThreads = 256, kAppendWarps = kAppendThreads / 32;
 // CTAs an SM for all but the largest blocks: more hide more of that latency (16022 tokens: 19.6 us with 5,
 // 18.9 with 6; the same chain took 24.5 with 4).

@@ -15,7 +15,8 @@
  *   - Scores, softmax statistics and accumulators are float32. The probabilities enter the second product rounded to the
  *     operands' type (decode: to f16), unnormalised; the sum that divides them is taken before that rounding. Where that
  *     type is f16 they are scaled up first, so that a probability keeps f16's 11 bits down to 2^-21 (decode: 2^-29) of the
- *     row's largest; below that it is off by up to 2^-32 (2^-40) of the largest.
+ *     row's largest; below that it is off by up to 2^-32 (2^-40) of the largest. Decode takes its queries as f16, each row
+ *     scaled by a power of two: exact down to 2^-28 of the row's largest.
  *   - Values in places that the mask hides (later keys, other sequences, slots past a request's length) have no
  *     influence, NaN and infinities included.
  *   - Lengths, offsets, block ids and slots on the device are not trusted: what lies outside the buffers is left out.
